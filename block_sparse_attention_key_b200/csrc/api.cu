@@ -484,6 +484,29 @@ int qsa_forward(const qsa_dims* dims, const qsa_forward_args* a, void* workspace
                                      true));
 }
 
+// ---------------------------------------------------------------- whole prompts
+
+int qsa_prompt_attn(const qsa_dims* dims, const qsa_prompt_args* a, void* workspace, void* stream)
+{
+    int rc = check_dims(dims);
+    if (rc != QSA_OK) return rc;
+    if (!a || a->n_tok < 0) return QSA_ERR_INVALID_ARG;
+    if (workspace && !aligned16(workspace)) return QSA_ERR_INVALID_ARG;
+    // a token's heads are kHeadDim apart; tokens a whole number of 16-byte chunks
+    const int64_t q_row = (int64_t)dims->n_q_heads * kHeadDim, kv_row = (int64_t)dims->n_kv_heads * kHeadDim;
+    if (a->q_ld < q_row || a->k_ld < kv_row || a->v_ld < kv_row || a->q_ld % 8 || a->k_ld % 8 || a->v_ld % 8)
+        return QSA_ERR_INVALID_ARG;
+    if (a->n_tok == 0) return QSA_OK;
+    if (!aligned16(a->q) || !aligned16(a->k) || !aligned16(a->v) || !aligned16(a->cu_len) || !aligned16(a->out))
+        return QSA_ERR_INVALID_ARG;
+    // TMA coordinates and the grid are 32-bit, token strides 40-bit
+    if (a->n_tok > (1 << 30) || prompt_attn_ctas(*dims, a->n_tok) > INT32_MAX || a->q_ld >= (1ll << 38) ||
+        a->k_ld >= (1ll << 38) || a->v_ld >= (1ll << 38))
+        return QSA_ERR_UNSUPPORTED;
+    return cuda_status(launch_prompt_attn(*dims, a->q, a->q_ld, a->k, a->k_ld, a->v, a->v_ld, a->cu_len, a->n_tok,
+                                          a->out, (unsigned*)workspace, (cudaStream_t)stream));
+}
+
 // ---------------------------------------------------------------- context parallelism
 
 static int check_shard(const qsa_dims* shard, int32_t n_q, int64_t blk_lo)

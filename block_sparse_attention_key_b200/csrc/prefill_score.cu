@@ -48,11 +48,9 @@
 
 #include <atomic>
 #include <cfloat>
-#include <mutex>
-
-#include <cudaTypedefs.h>
 
 #include "select_finish.cuh"
+#include "sm100_host.cuh"
 #include "sm100_ptx.cuh"
 
 namespace qsa {
@@ -71,7 +69,6 @@ constexpr int kHistBins = 64;
 constexpr int kHistShift = 19;          // main pass: 1/16-octave bins of the orderable key
 constexpr int kSampleShift = 19;        // sampling pass: 1/16-octave bins (a 4-octave window)
 constexpr int kRaiseEvery = 32;         // admissions between threshold updates
-constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s bound on any single wait
 constexpr int kSampleStride = 16;
 constexpr int kSampleKth = 64;
 constexpr int kShistWords = kHistBins + 1;   // per (row, CTA, warpgroup): window base, then counts
@@ -94,35 +91,6 @@ struct __align__(1024) K3Smem {
     int error;
 };
 
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Bounded wait: polls until the phase completes, the CTA's error flag is set, or
-// kWaitNs passes (then sets the flag).  Returns true only if the phase completed.
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* error, unsigned* status)
-{
-    if (mbar_try_wait(bar, parity)) return true;  // fast path: no timer read
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 255u) == 0u) {
-            if (*error) return false;
-            const uint64_t t = now_ns();
-            if (t0 == 0) {
-                t0 = t;
-            } else if (t - t0 > kWaitNs) {
-                *error = 1;
-                set_status(status, QSA_DEV_TIMEOUT);
-                return false;
-            }
-        }
-    }
-}
-
 // v[c] for a run-time c without local memory: a 5-level tree of selects.
 __device__ __forceinline__ float pick32(const float (&v)[32], int c)
 {
@@ -141,25 +109,6 @@ __device__ __forceinline__ float pick32(const float (&v)[32], int c)
 __device__ __forceinline__ float key_to_float(unsigned k)
 {
     return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
-}
-
-__device__ __forceinline__ unsigned long long pack2(float lo, float hi)
-{
-    return ((unsigned long long)__float_as_uint(hi) << 32) | __float_as_uint(lo);
-}
-
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c)
-{
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c)
-{
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
 }
 
 // 32 consecutive TMEM columns of this thread's lane (two 16-column loads; the caller waits).
@@ -758,37 +707,6 @@ k_prefill_fallback(const __nv_bfloat16* __restrict__ q_idx, const float* __restr
 }
 
 // ---------------------------------------------------------------- host side
-
-namespace {
-
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
-{
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-bool set_smem_once(const void* fn, int bytes, std::atomic<bool> (&done)[128])
-{
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 128) return false;
-    if (!done[dev].load()) {  // setting it twice (two host threads) is harmless
-        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-        done[dev].store(true);
-    }
-    return true;
-}
-
-}  // namespace
-
 int prefill_splits(int32_t n_q, int64_t max_blocks)
 {
     const int n_tiles = (n_q + kM - 1) / kM;

@@ -197,6 +197,12 @@ cudaError_t launch_sparse_attn(const qsa_dims& d, const void* q, const void* k_c
                                unsigned* status, cudaStream_t st, bool pdl, bool allow_cluster,
                                bool counters_zeroed, float* part_out = nullptr);
 
+// Causal attention over packed whole prompts (prompt_attn.cu).  ld: elements between tokens.
+int64_t prompt_attn_ctas(const qsa_dims& d, int32_t n_tok);
+cudaError_t launch_prompt_attn(const qsa_dims& d, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                               const void* v, int64_t v_ld, const int32_t* cu_len, int32_t n_tok, void* out,
+                               unsigned* status, cudaStream_t st);
+
 // Context-parallel steps (cp.cu).
 size_t cp_partial_row_floats();
 cudaError_t launch_cp_local_pos(const int32_t* q_pos, int32_t n_q, int64_t tok_lo, int64_t cap_loc, int32_t* pos_loc,

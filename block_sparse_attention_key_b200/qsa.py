@@ -38,7 +38,7 @@ EXPORTED = (
     "qsa_pool_block_keys", "qsa_index_scores", "qsa_topk_blocks", "qsa_sparse_attn", "qsa_forward",
     "qsa_sparse_attn_noalloc", "qsa_sparse_attn_ex", "qsa_select_blocks",
     "qsa_cp_workspace_bytes", "qsa_cp_select_keys", "qsa_cp_merge_keys", "qsa_cp_attn_partial", "qsa_cp_combine",
-    "qsa_attn_plan",
+    "qsa_attn_plan", "qsa_prompt_attn",
 )
 
 CP_PART_ROW = 132  # floats per (query, head) partial of a context shard
@@ -90,6 +90,14 @@ class qsa_attn_plan_info(ctypes.Structure):
     ]
 
 
+class qsa_prompt_args(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_ld", ctypes.c_int64),
+        ("k_ld", ctypes.c_int64), ("v_ld", ctypes.c_int64), ("cu_len", ctypes.c_void_p), ("n_tok", ctypes.c_int32),
+        ("out", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -124,6 +132,7 @@ def load(path=LIB_PATH):
     L.qsa_cp_attn_partial.argtypes = [D, P, P, P, P, P, I32, I64, P, P, P, P, SZ, P]
     L.qsa_cp_combine.argtypes = [D, I32, P, I32, P, P]
     L.qsa_attn_plan.argtypes = [D, I32, I32, ctypes.POINTER(qsa_attn_plan_info)]
+    L.qsa_prompt_attn.argtypes = [D, ctypes.POINTER(qsa_prompt_args), P, P]
     for name in EXPORTED:
         if name not in ("qsa_workspace_bytes", "qsa_status_string", "qsa_cp_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
@@ -251,6 +260,49 @@ def qsa_forward(dims, *, q, k_cache, v_cache, idx_k, pooled, q_idx, w, len_befor
                             _ptr(page_table), page_tokens, n_pages, n_decode)
     _check("qsa_forward", load().qsa_forward(ctypes.byref(dims), ctypes.byref(args), _ptr(workspace),
                                              workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- whole prompts
+
+def _like(name, t, dtype, shape):
+    """Type and shape of an argument (the C ABI cannot see either)."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+
+
+def _here(*tensors):
+    """Launches go to the current device: every tensor has to lie there."""
+    import torch
+    dev = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else None
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != dev:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+
+
+def _token_rows(name, t, n_tok, heads):
+    """Pointer and token stride of bf16 [n_tok][heads][128], heads dense, tokens any stride."""
+    if not t.is_cuda:
+        raise ValueError("libqsa takes CUDA tensors only (no CPU path)")
+    if n_tok and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != 128)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), t.stride(0) if n_tok > 1 else heads * 128
+
+
+def qsa_prompt_attn(dims, q, k, v, cu_len, n_tok, out, workspace=None, stream=None):
+    """Causal attention over packed whole prompts.  q, k, v: bf16 [n_tok][heads][128], also as
+    slices of a fused projection; cu_len: i32 [batch + 1]; out: bf16 [n_tok][n_q_heads][128]."""
+    import torch
+    for name, t, heads in (("q", q, dims.n_q_heads), ("k", k, dims.n_kv_heads), ("v", v, dims.n_kv_heads),
+                           ("out", out, dims.n_q_heads)):
+        _like(name, t, torch.bfloat16, (n_tok, heads, 128))
+    _like("cu_len", cu_len, torch.int32, (dims.batch + 1,))
+    qp, q_ld = _token_rows("q", q, n_tok, dims.n_q_heads)
+    kp, k_ld = _token_rows("k", k, n_tok, dims.n_kv_heads)
+    vp, v_ld = _token_rows("v", v, n_tok, dims.n_kv_heads)
+    _here(q, k, v, cu_len, out, workspace)
+    args = qsa_prompt_args(qp, kp, vp, q_ld, k_ld, v_ld, _ptr(cu_len), n_tok, _ptr(out))
+    _check("qsa_prompt_attn", load().qsa_prompt_attn(ctypes.byref(dims), ctypes.byref(args), _ptr(workspace),
+                                                     _stream(stream)))
 
 
 # ---------------------------------------------------------------- context parallelism (see include/qsa.h)

@@ -306,6 +306,36 @@ typedef struct qsa_forward_args {
 int qsa_forward(const qsa_dims* dims, const qsa_forward_args* args, void* workspace,
                 size_t ws_bytes, void* stream);
 
+/* ---- whole prompts: dense causal attention, packed ----
+ *
+ * out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h].k[j][g]) v[j][g], j over the tokens
+ * of query token i's own sequence: what the layer computes while a prompt is shorter
+ * than its budget, and what a model's dense GQA layers compute at any length.  fp32
+ * logits, softmax and accumulation; bf16 output (RNE).
+ *
+ * Sequence s (of dims.batch) owns tokens [cu_len[s], cu_len[s+1]) of the packed arrays;
+ * empty sequences are allowed.  Tokens before cu_len[0] and from cu_len[batch] on belong
+ * to nobody: they are neither attended nor written.  A sequence whose bounds decrease or
+ * leave [0, n_tok] is skipped and QSA_DEV_BAD_LEN set.
+ * q, k and v may be slices of a wider array (a fused projection's output): head h of
+ * token i starts at element i * ld + h * head_dim, ld a multiple of 8 and at least
+ * n_heads * head_dim.  `out` must not overlap them.
+ * A token that a query must not see has no influence on it, whatever it holds (NaN and
+ * infinities included).
+ * dims: batch, n_q_heads, n_kv_heads, head_dim, softmax_scale are used; the others only
+ * have to be valid.  workspace: may be NULL (then device errors are not reported). */
+typedef struct qsa_prompt_args {
+    const void* q;          /* bf16 [n_tok][q_ld], heads packed */
+    const void* k;          /* bf16 [n_tok][k_ld] */
+    const void* v;          /* bf16 [n_tok][v_ld] */
+    int64_t q_ld, k_ld, v_ld; /* elements from token to token */
+    const int32_t* cu_len;  /* i32 [batch + 1] */
+    int32_t n_tok;          /* rows of the packed arrays */
+    void* out;              /* bf16 [n_tok][n_q_heads][head_dim] */
+} qsa_prompt_args;
+
+int qsa_prompt_attn(const qsa_dims* dims, const qsa_prompt_args* args, void* workspace, void* stream);
+
 /* ---- context parallelism: one sequence's blocks spread over several GPUs ----
  *
  * ai-manual.ru, discussion of llama.cpp PR #30965 (closing note): several GPUs add
