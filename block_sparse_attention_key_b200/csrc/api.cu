@@ -484,6 +484,69 @@ int qsa_forward(const qsa_dims* dims, const qsa_forward_args* a, void* workspace
                                      true));
 }
 
+// ---------------------------------------------------------------- caches in 4 bits
+
+static int check_kv4(const qsa_dims* d, const qsa_kv4_cache* c)
+{
+    if (!c) return QSA_ERR_INVALID_ARG;
+    return check_pages(d, c->page_table, c->page_tokens, c->n_pages);
+}
+
+static bool kv4_aligned(const qsa_kv4_cache* c)
+{
+    return aligned16(c->k_codes) && aligned16(c->k_scales) && aligned16(c->v_codes) && aligned16(c->v_scales);
+}
+
+int qsa_kv4_append(const qsa_dims* dims, const qsa_kv4_cache* cache, const void* k, int64_t k_ld, const void* v,
+                   int64_t v_ld, const int32_t* cu_len, const int32_t* len_before, int32_t n_tok, void* workspace,
+                   void* stream)
+{
+    int rc = check_dims(dims);
+    if (rc != QSA_OK) return rc;
+    if ((rc = check_kv4(dims, cache)) != QSA_OK) return rc;
+    if (n_tok < 0 || (workspace && !aligned16(workspace))) return QSA_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)dims->n_kv_heads * kHeadDim;
+    if (k_ld < row || v_ld < row || k_ld % 8 || v_ld % 8) return QSA_ERR_INVALID_ARG;
+    if (n_tok == 0) return QSA_OK;
+    if (!kv4_aligned(cache) || !aligned16(k) || !aligned16(v) || !aligned16(cu_len) || !aligned16(len_before))
+        return QSA_ERR_INVALID_ARG;
+    if ((int64_t)n_tok * dims->n_kv_heads > (1ll << 33)) return QSA_ERR_UNSUPPORTED;  // 16 rows of threads per CTA
+    return cuda_status(launch_kv4_append(*dims, *cache, k, k_ld, v, v_ld, cu_len, len_before, n_tok,
+                                         (unsigned*)workspace, (cudaStream_t)stream));
+}
+
+int qsa_sparse_attn_kv4(const qsa_dims* dims, const qsa_kv4_cache* cache, const qsa_attn_args* a, void* workspace,
+                        void* stream)
+{
+    int rc = check_dims(dims);
+    if (rc != QSA_OK) return rc;
+    if ((rc = check_kv4(dims, cache)) != QSA_OK) return rc;
+    if (!a || a->k_cache || a->v_cache || a->page_table || a->page_tokens || a->n_pages) return QSA_ERR_INVALID_ARG;
+    if ((rc = check_rows(dims, a->n_q, 0)) != QSA_OK) return rc;
+    if ((rc = check_groups(dims, a->n_q, a->group_q < 1 ? 0 : a->group_q)) != QSA_OK) return rc;
+    if (workspace && !aligned16(workspace)) return QSA_ERR_INVALID_ARG;
+    if (a->n_q == 0) return QSA_OK;
+    if (!kv4_aligned(cache) || !aligned16(a->q) || !aligned16(a->q_seq) || !aligned16(a->q_pos) ||
+        !aligned16(a->sel_idx) || !aligned16(a->sel_cnt) || !aligned16(a->out))
+        return QSA_ERR_INVALID_ARG;
+    if (dims->n_kv_heads > 65535) return QSA_ERR_UNSUPPORTED;  // KV heads index a grid dimension
+    return cuda_status(launch_sparse_attn_kv4(*dims, *cache, a->q, a->q_seq, a->q_pos, a->sel_idx, a->sel_cnt,
+                                              a->n_q / a->group_q, a->group_q, a->out, (unsigned*)workspace,
+                                              (cudaStream_t)stream));
+}
+
+int qsa_attn_kv4_plan(const qsa_dims* dims, int32_t n_q, int32_t group_q, qsa_attn_plan_info* info)
+{
+    int rc = check_dims(dims);
+    if (rc != QSA_OK) return rc;
+    if (!info) return QSA_ERR_INVALID_ARG;
+    if ((rc = check_rows(dims, n_q, 0)) != QSA_OK) return rc;
+    if ((rc = check_groups(dims, n_q, group_q < 1 ? 0 : group_q)) != QSA_OK) return rc;
+    *info = qsa_attn_plan_info{};
+    if (n_q > 0) plan_kv4(*dims, n_q / group_q, group_q, info);
+    return QSA_OK;
+}
+
 // ---------------------------------------------------------------- whole prompts
 
 int qsa_prompt_attn(const qsa_dims* dims, const qsa_prompt_args* a, void* workspace, void* stream)

@@ -1,0 +1,765 @@
+// Gathered GQA attention (step 4 of the QSA layer) over a cache held in 4 bits: rows of
+// 128 values as 64 bytes of e2m1 codes and 8 e4m3 scales, one per 16 values,
+//     k[d] = e2m1(code[d]) * e4m3(scale[d / 16])         (144 bytes of K and V per token
+// and KV head instead of 512).  Same selections, draft groups, pages and results as the
+// bf16 call over the cache's values.
+//
+// Arithmetic: a product of an e2m1 and an e4m3 number has at most 6 significant bits
+// between 2^-10 and 2688, so it is exact in fp16; the hardware turns a byte of codes
+// into two fp16 values and one packed multiply applies the scale.  Queries become fp16
+// after a per-row power of two brings their largest magnitude to [2^14, 2^15) (a bf16
+// value then keeps every bit down to 2^-31 of the row's largest, and errs by 2^-39 of it
+// below); the power is undone in the logits' fp32 scale.  Probabilities are rounded to
+// fp16 times 2^14 (11 bits; those below 2^-28 of the running maximum lose bits one by
+// one), the sum keeps the unrounded ones.  fp32 accumulation throughout.
+//
+// Work unit, splits and pipeline: one CTA per (split, KV head, draft group), its rows the
+// group's query heads of that KV head (<= 32), tokens on the M side of mma.sync m16n8k16.
+// The splits of a (group, KV head) form one thread-block cluster and merge in its first
+// CTA's shared memory, so a call needs no scratch.  What differs from a bf16 gather is
+// that unpacking, not the copies, is the work: operands never pass through shared memory
+// unpacked.  The contraction's order is free, so a lane takes 32 consecutive dims of its
+// K rows (one 16-byte shared load = all A fragments of a row, the query fragments use the
+// same order), and 16 consecutive dims of its four V tokens (8 bytes and one scale each);
+// V pairs are two tokens of one dim: their nibbles are interleaved with bit selects
+// before the conversion (4 logic operations per 16 values).
+//
+// Masked places: absent tokens are zero-filled and their logits -inf.  A scale may be NaN
+// (the append writes that for values that are not finite): a draft's tail token that is
+// not visible to an earlier draft of its group must not reach it through 0 x NaN, so
+// such groups are zeroed and the NaN is added to the rows that see the token.
+
+#include <atomic>
+#include <climits>
+#include <mutex>
+
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+
+#include "qsa_internal.cuh"
+
+namespace qsa {
+
+namespace {
+
+constexpr int kTok4 = 64;                      // tokens per stage
+constexpr int kCodeRow = kHeadDim / 2;         // 64 B of codes per token row
+constexpr int kScaleRow = kHeadDim / 16;       // 8 B of scales per token row
+constexpr int kCodes = kTok4 * kCodeRow;       // 4 KiB of K (or V) codes per stage
+constexpr int kScales = kTok4 * kScaleRow;
+constexpr int kStage4 = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
+constexpr int kItems4 = kSelCap + 2;           // selected blocks + up to 2 tail blocks
+constexpr int kItemCap4 = 592;                 // items of one split, in whole stages
+constexpr int kMaxStages4 = 16;
+constexpr int kMaxSplits4 = 16;                // one cluster
+constexpr float kProbShift = 14.0f;            // probabilities are held times 2^14
+
+struct Layout4 {
+    int q, stage, tok, ioff, ipos, rowt, rows, total;
+};
+__host__ __device__ inline Layout4 layout4(int rp, int stages)
+{
+    Layout4 L;
+    L.q = 0;
+    L.stage = rp * kHeadDim * 2;
+    L.tok = L.stage + stages * kStage4;
+    L.ioff = L.tok + stages * kTok4 * 4;
+    L.ipos = L.ioff + kItemCap4 * 8;
+    L.rowt = L.ipos + kItemCap4 * 4;
+    L.rows = L.rowt + 32 * 4;
+    L.total = L.rows + 32 * 4;
+    return L;
+}
+
+__device__ __forceinline__ uint32_t swz_q(int row, int chunk)
+{
+    return (uint32_t)(row * (kHeadDim * 2) + ((chunk ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t saddr, const void* g, int src_bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(saddr), "l"(g), "r"(src_bytes));
+}
+__device__ __forceinline__ void cp_async8(uint32_t saddr, const void* g, int src_bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(saddr), "l"(g), "r"(src_bytes));
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::); }
+__device__ __forceinline__ void cp_wait_pending(int n)
+{
+    // wait until at most n committed groups are still in flight (n < kMaxStages4)
+    switch (n) {
+#define QSA_WAIT(i) case i: asm volatile("cp.async.wait_group " #i ";\n" ::); break
+    QSA_WAIT(0); QSA_WAIT(1); QSA_WAIT(2); QSA_WAIT(3); QSA_WAIT(4); QSA_WAIT(5); QSA_WAIT(6); QSA_WAIT(7);
+    QSA_WAIT(8); QSA_WAIT(9); QSA_WAIT(10); QSA_WAIT(11); QSA_WAIT(12); QSA_WAIT(13); QSA_WAIT(14);
+#undef QSA_WAIT
+    default: asm volatile("cp.async.wait_group 15;\n" ::); break;
+    }
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(a));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t movm_t(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the four bytes of w, each two e2m1 codes (low half first) -> four packed fp16 pairs
+__device__ __forceinline__ void unpack_e2m1x8(uint32_t w, uint32_t (&h)[4])
+{
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+// two e4m3 bytes (low 16 bits) -> packed fp16 pair
+__device__ __forceinline__ uint32_t unpack_e4m3x2(uint32_t b)
+{
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"((uint16_t)b));
+    return h;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+}  // namespace
+
+// NT = 8-row column tiles of the MMA's N side (rows = drafts x G <= 8 * NT); NWG = groups
+// of 4 compute warps, each group taking every NWG-th stage with its own softmax state.
+template <int NT, int NWG>
+__global__ void __launch_bounds__(128 * NWG)
+k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_codes,
+                  const uint8_t* __restrict__ k_scales, const uint8_t* __restrict__ v_codes,
+                  const uint8_t* __restrict__ v_scales, const int32_t* __restrict__ q_seq,
+                  const int32_t* __restrict__ q_pos, const int32_t* __restrict__ sel_idx,
+                  const int32_t* __restrict__ sel_cnt, const int32_t* __restrict__ page_table, int page_tokens,
+                  int64_t table_ld, int64_t n_pages, int batch, int n_q_heads, int n_kv_heads, int64_t kv_capacity,
+                  int bs_log2, int top_k, int group_q, float scale_log2, int items_per_split, int n_split,
+                  int n_stages, __nv_bfloat16* __restrict__ out, unsigned* status)
+{
+    constexpr int RP = 8 * NT;           // padded rows
+    constexpr int kT = 128 * NWG;        // threads
+    constexpr int kW = 4 * NWG;          // warps
+    constexpr int kPerT = (kItemCap4 + kT - 1) / kT;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int s_cnt, s_nitems, s_seq, s_nc0, s_tlast;
+    const Layout4 SL = layout4(RP, n_stages);
+    const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
+    int* s_tok = reinterpret_cast<int*>(smem + SL.tok);
+    long long* s_ioff = reinterpret_cast<long long*>(smem + SL.ioff);
+    int* s_ipos = reinterpret_cast<int*>(smem + SL.ipos);
+    int* s_rowt = reinterpret_cast<int*>(smem + SL.rowt);
+    float* s_rows = reinterpret_cast<float*>(smem + SL.rows);
+
+    // grid (splits, KV heads, groups), or (groups, KV heads) for one CTA per pair
+    const bool one = n_split == 1;
+    const int split = one ? 0 : blockIdx.x, g = blockIdx.y, grp = one ? blockIdx.x : blockIdx.z;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int G = n_q_heads / n_kv_heads;
+    const int R = group_q * G;
+    const int64_t qi0 = (int64_t)grp * group_q;
+    const int bs = 1 << bs_log2;     // tokens per block
+    const int ipt = kTok4 >> bs_log2;  // blocks per stage
+
+    // ---- one round of independent loads: positions, queries, this split's selection ----
+    const int a0 = split * items_per_split;
+    int raw[kPerT];
+#pragma unroll
+    for (int u = 0; u < kPerT; ++u) {
+        const int k = tid + u * kT;
+        const int a = a0 + k;
+        raw[u] = (k < items_per_split && a < kSelCap) ? __ldg(sel_idx + (int64_t)grp * kSelCap + a) : -1;
+    }
+    const int cnt_raw = tid == 0 ? __ldg(sel_cnt + grp) : 0;
+    if (warp == 0) {
+        // lane r < RP: row r = (draft query j = r / G, head r % G); its position, or -2
+        const int s0 = q_seq[qi0], t0 = q_pos[qi0];
+        const bool ok0 = s0 >= 0 && s0 < batch && t0 >= 0 && (int64_t)t0 < kv_capacity;
+        const int nc0 = ok0 ? (int)(((int64_t)t0 + 1) >> bs_log2) : 0;
+        int t = -2;
+        if (lane < R && ok0) {
+            const int j = lane / G;
+            const int sj = q_seq[qi0 + j], tj = q_pos[qi0 + j];
+            // a draft query follows the selection's query within the two tail blocks
+            const bool ok = sj == s0 && tj >= t0 && (int64_t)tj <= (int64_t)bs * nc0 + 2 * bs - 1 &&
+                            (int64_t)tj < kv_capacity;
+            if (ok) t = tj;
+            else if (split == 0 && g == 0 && lane % G == 0)
+                set_status(status, sj != s0 ? QSA_DEV_BAD_SEQ : QSA_DEV_BAD_POS);
+        }
+        if (lane < RP) s_rowt[lane] = t;
+        const int tl = __reduce_max_sync(0xffffffffu, lane < R ? t : -2);
+        if (lane == 0) {
+            s_seq = ok0 ? s0 : -1;
+            s_nc0 = nc0;
+            s_tlast = tl;
+            if (!ok0 && split == 0 && g == 0)
+                set_status(status, (s0 < 0 || s0 >= batch) ? QSA_DEV_BAD_SEQ : QSA_DEV_BAD_POS);
+        }
+    }
+    // query rows in fp16, 16 threads per row: the row's largest magnitude goes to [2^14, 2^15)
+    for (int k = tid; k < RP * 16; k += kT) {
+        const int row = k >> 4, ch = k & 15;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < R) v = __ldg(q + ((qi0 + row / G) * n_q_heads + (int64_t)g * G + row % G) * 16 + ch);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t top = 0;            // largest exponent field (bits 14..7 of a bf16)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7F80u, (w[e] >> 16) & 0x7F80u));
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // exponent e (value 2^(e - 127) to 2^(e - 126)): times 2^(141 - e), kept a normal fp32 number
+        const int up = min(max(141 - (int)(top >> 7), -113), 100);
+        const float f = __int_as_float((127 + up) << 23);
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = pack_f16(bf16lo(w[e]) * f, bf16hi(w[e]) * f);
+        *reinterpret_cast<uint4*>(smem + swz_q(row, ch)) = make_uint4(h[0], h[1], h[2], h[3]);
+        if (ch == 0) s_rows[row] = __int_as_float((127 - up) << 23) * scale_log2;
+    }
+    __syncthreads();  // s_seq, s_nc0, s_tlast, s_rowt, query rows
+    if (tid == 0) {
+        int cnt = s_seq >= 0 ? cnt_raw : 0;
+        const int cnt_max = min(s_nc0, top_k);
+        if (cnt < 0 || cnt > cnt_max) {
+            if (split == 0 && g == 0) set_status(status, QSA_DEV_BAD_SEL);
+            cnt = cnt < 0 ? 0 : cnt_max;
+        }
+        const int tl = s_tlast;
+        const int64_t tail0 = (int64_t)bs * s_nc0;
+        const int n_tail = tl >= tail0 ? (int)((tl - tail0) >> bs_log2) + 1 : 0;
+        s_cnt = cnt;
+        s_nitems = cnt + n_tail;
+    }
+    __syncthreads();
+    const int cnt = s_cnt;
+    const int n_blk = max(0, min(a0 + items_per_split, s_nitems) - a0);
+    const int s = s_seq;
+    const int nc0 = s_nc0;
+#pragma unroll
+    for (int u = 0; u < kPerT; ++u) {
+        const int k = tid + u * kT;
+        if (k >= n_blk) continue;
+        const int a = a0 + k;
+        int p0 = -1, ipos = -1;  // first token of the item; ipos -1: visible to every row
+        if (a < cnt) {
+            const int b = raw[u];
+            if (b >= 0 && b < nc0) p0 = b << bs_log2;
+            else set_status(status, QSA_DEV_BAD_SEL);
+        } else {
+            p0 = (nc0 + (a - cnt)) << bs_log2;
+            ipos = p0;
+        }
+        long long off = -1;      // token row in the cache
+        if (p0 >= 0) {
+            if (page_table) {
+                const int page = __ldg(page_table + (int64_t)s * table_ld + p0 / page_tokens);
+                if (page >= 0 && page < n_pages)
+                    off = ((long long)page * n_kv_heads + g) * page_tokens + p0 % page_tokens;
+                else
+                    set_status(status, QSA_DEV_BAD_PAGE);
+            } else {
+                off = ((long long)s * n_kv_heads + g) * kv_capacity + p0;
+            }
+        }
+        s_ioff[k] = off;
+        s_ipos[k] = ipos;
+    }
+    __syncthreads();
+
+    const int tlast = s_tlast;
+    const int n_tiles = (n_blk + ipt - 1) / ipt;
+    // four threads per token row, each copying one 16-byte chunk of K and one of V codes;
+    // the first two also the row's K and V scales
+    constexpr int kRowsPerPass = kT / 4;
+    auto load_tile = [&](int tile, int slot) {
+        const int q4 = tid & 3;
+        const uint32_t st = sbase + SL.stage + slot * kStage4;
+#pragma unroll
+        for (int u = 0; u < kTok4 / kRowsPerPass; ++u) {
+            const int row = (tid >> 2) + u * kRowsPerPass;
+            const int it = tile * ipt + (row >> bs_log2);
+            const int tin = row & (bs - 1);
+            long long off = -1;
+            int tp = INT_MAX;
+            if (it < n_blk) {
+                off = s_ioff[it];
+                const int ip = s_ipos[it];
+                if (off >= 0 && ip >= 0 && ip + tin > tlast) off = -1;  // past the group's last draft token
+                if (off >= 0) tp = ip < 0 ? -1 : ip + tin;
+            }
+            const int n16 = off >= 0 ? 16 : 0, n8 = off >= 0 ? 8 : 0;
+            const long long e = off >= 0 ? off + tin : 0;
+            // token tt of a warp's 16: K in the order the MMA rows read it, V by token with
+            // the chunk's upper bit flipped every two tokens (both reads without conflicts)
+            const int grp16 = row >> 4, tt = row & 15;
+            const uint32_t kpos = grp16 * 1024 + ((tt & 3) + ((tt >> 3) << 2)) * 128 + ((tt >> 2) & 1) * 64 + q4 * 16;
+            const uint32_t vpos = kCodes + row * 64 + ((q4 ^ (tt & 2)) << 4);
+            cp_async16(st + kpos, k_codes + e * kCodeRow + q4 * 16, n16);
+            cp_async16(st + vpos, v_codes + e * kCodeRow + q4 * 16, n16);
+            if (q4 == 0) cp_async8(st + 2 * kCodes + row * 8, k_scales + e * kScaleRow, n8);
+            if (q4 == 1) cp_async8(st + 2 * kCodes + kScales + row * 8, v_scales + e * kScaleRow, n8);
+            if (q4 == 0) s_tok[slot * kTok4 + row] = tp;
+        }
+    };
+
+    // every slot is filled at once; later tiles refill the slots of a finished round
+    int issued = 0;
+    for (; issued < n_stages && issued < n_tiles; ++issued) {
+        load_tile(issued, issued);
+        cp_commit();
+    }
+
+    const int wg = warp >> 2;        // compute group
+    const int wq = warp & 3;         // warp within the group: 16 tokens of the stage
+    const int c4 = lane & 3, l4 = lane >> 2;
+    int trow[NT][2];
+    float rsc[NT][2];                // logit scale of the lane's accumulator columns
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            trow[nt][j] = s_rowt[8 * nt + 2 * c4 + j];
+            rsc[nt][j] = s_rows[8 * nt + 2 * c4 + j];
+        }
+    // Q^T fragments (B operand: k = dims, n = rows): the lane holds dims 32 c4 .. 32 c4 + 31 of
+    // row 8 nt + l4, 4 dims per k-step; in registers for NT <= 2
+    constexpr bool kHoldQ = NT <= 2;
+    uint32_t qb[kHoldQ ? 4 : 1][NT][4];
+    if constexpr (kHoldQ) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 v = lds128(sbase + swz_q(8 * nt + l4, 4 * c4 + w));
+                qb[w][nt][0] = v.x, qb[w][nt][1] = v.y, qb[w][nt][2] = v.z, qb[w][nt][3] = v.w;
+            }
+    }
+
+    float o[8][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+    const int tt_lo = (l4 >> 1) + ((l4 & 1) << 2);   // token (of 16) of MMA row l4; row l4 + 8 holds tt_lo + 8
+
+    for (int r0 = 0; r0 < n_tiles; r0 += NWG) {
+        // tiles r0 .. r0 + NWG - 1 have landed (this thread's copies), then every thread's
+        const int done = min(n_tiles, r0 + NWG);
+        cp_wait_pending(issued - done);
+        __syncthreads();
+        const int tile = r0 + wg;
+        const int slot = tile % n_stages;
+        const uint32_t st = sbase + SL.stage + slot * kStage4;
+        const bool have = tile < n_tiles;
+        const int tp0 = have ? s_tok[slot * kTok4 + 16 * wq + tt_lo] : INT_MAX;
+        const int tp1 = have ? s_tok[slot * kTok4 + 16 * wq + tt_lo + 8] : INT_MAX;
+
+        if (__any_sync(0xffffffffu, tp0 != INT_MAX || tp1 != INT_MAX)) {  // skip a warp's empty tokens
+            // ---- S^T = K Q^T: rows l4 and l4 + 8, dims 32 c4 + 8 w .. + 7 per word ----
+            float sa[NT][4], sb[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sa[nt][e] = sb[nt][e] = 0.f;
+            const uint4 k0 = lds128(st + wq * 1024 + l4 * 64 + c4 * 16);
+            const uint4 k1 = lds128(st + wq * 1024 + 512 + l4 * 64 + c4 * 16);
+            const uint32_t ksc = st + 2 * kCodes + (16 * wq + tt_lo) * 8 + 2 * c4;
+            const uint32_t s0 = unpack_e4m3x2(lds16(ksc)), s1 = unpack_e4m3x2(lds16(ksc + 64));
+            const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                // words 0 and 1 lie in the lane's first scale group, 2 and 3 in its second
+                const uint32_t f0 = __byte_perm(s0, s0, w < 2 ? 0x1010 : 0x3232);
+                const uint32_t f1 = __byte_perm(s1, s1, w < 2 ? 0x1010 : 0x3232);
+                uint32_t h0[4], h1[4];
+                unpack_e2m1x8(kw0[w], h0);
+                unpack_e2m1x8(kw1[w], h1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    h0[e] = mul_f16x2(h0[e], f0);
+                    h1[e] = mul_f16x2(h1[e], f1);
+                }
+                const uint32_t ka[4] = {h0[0], h1[0], h0[1], h1[1]};
+                const uint32_t kb[4] = {h0[2], h1[2], h0[3], h1[3]};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if constexpr (kHoldQ) {
+                        mma16816_f16(sa[nt], ka, qb[w][nt][0], qb[w][nt][1]);
+                        mma16816_f16(sb[nt], kb, qb[w][nt][2], qb[w][nt][3]);
+                    } else {
+                        const uint4 v = lds128(sbase + swz_q(8 * nt + l4, 4 * c4 + w));
+                        mma16816_f16(sa[nt], ka, v.x, v.y);
+                        mma16816_f16(sb[nt], kb, v.z, v.w);
+                    }
+                }
+            }
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                // element e: token tt_lo (+8 for e >= 2), row 8nt + 2c4 + (e & 1)
+                float x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tp = e < 2 ? tp0 : tp1;
+                    x[e] = tp <= trow[nt][e & 1] ? (sa[nt][e] + sb[nt][e]) * rsc[nt][e & 1] : -INFINITY;
+                }
+                float a[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float mx = fmaxf(x[j], x[j + 2]);
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    const float mn = fmaxf(m[nt][j], mx);
+                    const float mu = mn == -INFINITY ? 0.f : mn;
+                    a[j] = exp2f(m[nt][j] - mu);
+                    const float p0 = exp2f(x[j] - mu + kProbShift), p1 = exp2f(x[j + 2] - mu + kProbShift);
+                    x[j] = p0;
+                    x[j + 2] = p1;
+                    l[nt][j] = l[nt][j] * a[j] + (p0 + p1);
+                    m[nt][j] = mn;
+                }
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                    o[mt][nt][0] *= a[0];
+                    o[mt][nt][1] *= a[1];
+                    o[mt][nt][2] *= a[0];
+                    o[mt][nt][3] *= a[1];
+                }
+                pb[nt][0] = movm_t(pack_f16(x[0], x[1]));  // MMA rows 0-7 -> B operand (k = token, n = row)
+                pb[nt][1] = movm_t(pack_f16(x[2], x[3]));  // rows 8-15
+            }
+            // ---- O^T += V^T P^T: tokens c4, c4 + 4 (k pair 0) and c4 + 8, c4 + 12 (k pair 1) ----
+            const int tv = 16 * wq + c4;
+            uint2 vw[4];
+            uint32_t vs[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int t = tv + 4 * u;
+                vw[u] = lds64(st + kCodes + t * 64 + (((l4 >> 1) ^ (t & 2)) << 4) + (l4 & 1) * 8);
+                vs[u] = lds8(st + 2 * kCodes + kScales + t * 8 + l4);
+            }
+            int bad = INT_MAX;       // first tail token whose group l4 is NaN
+            if (group_q > 1 && __any_sync(0xffffffffu, (tp0 >= 0 && tp0 != INT_MAX) || (tp1 >= 0 && tp1 != INT_MAX))) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int tp = s_tok[slot * kTok4 + tv + 4 * u];
+                    if (tp >= 0 && tp != INT_MAX && (vs[u] & 0x7Fu) == 0x7Fu) {
+                        bad = min(bad, tp);
+                        vs[u] = 0;
+                    }
+                }
+                bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 1));
+                bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 2));
+            }
+            const uint32_t g0 = unpack_e4m3x2(vs[0] | (vs[1] << 8)), g1 = unpack_e4m3x2(vs[2] | (vs[3] << 8));
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                // 8 dims 16 l4 + 8 half + i: nibble pairs (token A, token B) of dim i in byte order
+                const uint32_t a = half ? vw[0].y : vw[0].x, b = half ? vw[1].y : vw[1].x;
+                const uint32_t c = half ? vw[2].y : vw[2].x, d = half ? vw[3].y : vw[3].x;
+                constexpr uint32_t kLow = 0x0F0F0F0Fu;
+                uint32_t e0[4], e1[4], d0[4], d1[4];   // even dims, odd dims of the two token pairs
+                unpack_e2m1x8((a & kLow) | ((b << 4) & ~kLow), e0);
+                unpack_e2m1x8(((a >> 4) & kLow) | (b & ~kLow), d0);
+                unpack_e2m1x8((c & kLow) | ((d << 4) & ~kLow), e1);
+                unpack_e2m1x8(((c >> 4) & kLow) | (d & ~kLow), d1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // MMA row l4: dim 16 l4 + 2 mt, row l4 + 8: dim 16 l4 + 2 mt + 1
+                    const int mt = 4 * half + i;
+                    const uint32_t va[4] = {mul_f16x2(e0[i], g0), mul_f16x2(d0[i], g0), mul_f16x2(e1[i], g1),
+                                            mul_f16x2(d1[i], g1)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[mt][nt], va, pb[nt][0], pb[nt][1]);
+                }
+            }
+            if (__any_sync(0xffffffffu, bad != INT_MAX)) {
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (trow[nt][e & 1] >= bad) o[mt][nt][e] = __int_as_float(0x7FC00000);
+            }
+        }
+        __syncthreads();  // every warp is done with this round's slots
+        for (int u = 0; u < NWG && issued < n_tiles; ++u) {
+            load_tile(issued, issued % n_stages);
+            cp_commit();
+            ++issued;
+        }
+    }
+    cp_wait_pending(0);
+    __syncthreads();
+
+    // ---- merge the warps: (m, l) per row, O^T into shared memory (stage area) ----
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 4);
+            l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
+            l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
+        }
+    float* s_o = reinterpret_cast<float*>(smem + SL.stage);  // [kW][RP][128]
+    float* s_m = s_o + kW * RP * kHeadDim;                // [kW][RP]
+    float* s_l = s_m + kW * RP;                           // [kW][RP]
+    if (l4 == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                s_m[warp * RP + 8 * nt + 2 * c4 + j] = m[nt][j];
+                s_l[warp * RP + 8 * nt + 2 * c4 + j] = l[nt][j];
+            }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            // 16 consecutive dims of one row per lane
+            const int row = 8 * nt + 2 * c4 + j;
+            float* po = s_o + (warp * RP + row) * kHeadDim + 16 * l4;
+#pragma unroll
+            for (int mt = 0; mt < 8; mt += 2)
+                *reinterpret_cast<float4*>(po + 2 * mt) =
+                    make_float4(o[mt][nt][j], o[mt][nt][j + 2], o[mt + 1][nt][j], o[mt + 1][nt][j + 2]);
+        }
+    __syncthreads();
+
+    constexpr int TPR = kT / RP;          // threads per row
+    constexpr int DPT = kHeadDim / TPR;   // dims per thread: 4 .. 32
+    const int row = tid / TPR, d0 = (tid % TPR) * DPT;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) M = fmaxf(M, s_m[w * RP + row]);
+    const float Mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f, acc[DPT];
+#pragma unroll
+    for (int e = 0; e < DPT; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        const float f = exp2f(s_m[w * RP + row] - Mu);
+        L += s_l[w * RP + row] * f;
+#pragma unroll
+        for (int e = 0; e < DPT; ++e) acc[e] += s_o[(w * RP + row) * kHeadDim + d0 + e] * f;
+    }
+    const bool live_row = row < R;
+
+    if (n_split > 1) {
+        // the n_split CTAs of this (group, KV head) form one cluster: partials meet in
+        // the first CTA's shared memory; every thread of every CTA reaches both barriers
+        namespace cg = cooperative_groups;
+        cg::cluster_group cl = cg::this_cluster();
+        cl.sync();  // every CTA has finished its warp merge: stage areas are free
+        float* lead = cl.map_shared_rank(reinterpret_cast<float*>(smem + SL.stage), 0);
+        float* po = lead;                                       // [n_split][RP][128]
+        float* pm = lead + (size_t)n_split * RP * kHeadDim;     // [n_split][RP]
+        float* pl = pm + n_split * RP;                          // [n_split][RP]
+        if ((tid % TPR) == 0) {
+            pm[split * RP + row] = M;
+            pl[split * RP + row] = L;
+        }
+#pragma unroll
+        for (int e = 0; e < DPT; e += 4)
+            *reinterpret_cast<float4*>(po + (split * RP + row) * kHeadDim + d0 + e) =
+                make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        cl.sync();
+        if (split != 0 || !live_row) return;
+        const float* lpo = reinterpret_cast<const float*>(smem + SL.stage);
+        const float* lpm = lpo + (size_t)n_split * RP * kHeadDim;
+        const float* lpl = lpm + n_split * RP;
+        M = -INFINITY;
+        for (int sp = 0; sp < n_split; ++sp) M = fmaxf(M, lpm[sp * RP + row]);
+        const float mu = M == -INFINITY ? 0.f : M;
+        L = 0.f;
+#pragma unroll
+        for (int e = 0; e < DPT; ++e) acc[e] = 0.f;
+        for (int sp = 0; sp < n_split; ++sp) {
+            const float f = exp2f(lpm[sp * RP + row] - mu);
+            L += lpl[sp * RP + row] * f;
+#pragma unroll
+            for (int e = 0; e < DPT; e += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(lpo + (sp * RP + row) * kHeadDim + d0 + e);
+                acc[e] += v.x * f;
+                acc[e + 1] += v.y * f;
+                acc[e + 2] += v.z * f;
+                acc[e + 3] += v.w * f;
+            }
+        }
+    }
+    if (!live_row) return;
+    __nv_bfloat16* orow = out + ((qi0 + row / G) * n_q_heads + (int64_t)g * G + row % G) * kHeadDim + d0;
+    const float inv = L == 0.f ? 0.f : 1.f / L;   // a row that attends nothing is 0; a NaN sum stays NaN
+#pragma unroll
+    for (int e = 0; e < DPT; e += 4) {
+        uint2 v;
+        v.x = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+        v.y = pack_bf16(acc[e + 2] * inv, acc[e + 3] * inv);
+        *reinterpret_cast<uint2*>(orow + e) = v;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+namespace {
+
+int nt_for(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// compute groups: two for up to 16 rows; one for 32 (its accumulators fill the registers)
+int nwg_for(int nt) { return nt <= 2 ? 2 : 1; }
+
+const void* kernel4(int nt)
+{
+    return nt == 1 ? (const void*)k_sparse_attn_kv4<1, 2>
+                   : nt == 2 ? (const void*)k_sparse_attn_kv4<2, 2> : (const void*)k_sparse_attn_kv4<4, 1>;
+}
+
+bool configure4(int dev, int nt)
+{
+    static std::atomic<bool> done[64][3];
+    const int ni = nt == 1 ? 0 : nt == 2 ? 1 : 2;
+    if (dev < 0 || dev >= 64) return false;
+    if (done[dev][ni].load()) return true;
+    const void* fn = kernel4(nt);
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, layout4(8 * nt, kMaxStages4).total) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
+    done[dev][ni].store(true);
+    return true;
+}
+
+}  // namespace
+
+void plan_kv4(const qsa_dims& d, int64_t n_groups, int group_q, qsa_attn_plan_info* p)
+{
+    const int rows = d.n_q_heads / d.n_kv_heads * group_q;
+    const int nt = nt_for(rows), nwg = nwg_for(nt), rp = 8 * nt;
+    const int64_t pairs = n_groups * d.n_kv_heads;
+    const int ipt = kTok4 / d.block_size;
+    const int tiles_max = (kItems4 + ipt - 1) / ipt;
+    int ns = pairs >= 148 ? 1 : (int)(148 / pairs > kMaxSplits4 ? kMaxSplits4 : 148 / pairs);
+    if (ns > tiles_max) ns = tiles_max;
+    const int part = rp * (kHeadDim + 2) * 4;      // one split's partial in the merge buffer
+    if (ns * part > kMaxStages4 * kStage4) ns = kMaxStages4 * kStage4 / part;
+    const int tiles = (tiles_max + ns - 1) / ns;
+    ns = (tiles_max + tiles - 1) / tiles;          // no split without a tile
+    // few pairs: everything in flight at once; many: a short ring, several CTAs per SM
+    int st = ns == 1 && pairs >= 148 ? 4 : tiles < kMaxStages4 ? tiles : kMaxStages4;
+    if (st < 2 * nwg) st = 2 * nwg;
+    // the warps' (and the cluster's) merge buffers live in the stage area
+    const int merge = (ns > 4 * nwg ? ns : 4 * nwg) * part;
+    while (st * kStage4 < merge) ++st;
+    p->n_split = ns;
+    p->n_stages = st;
+    p->threads = 128 * nwg;
+    p->smem_bytes = layout4(rp, st).total;
+    p->ctas = pairs * ns;
+    p->cluster_merge = ns > 1;
+    p->rows = rows;
+}
+
+cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, const void* q, const int32_t* q_seq,
+                                   const int32_t* q_pos, const int32_t* sel_idx, const int32_t* sel_cnt,
+                                   int64_t n_groups, int group_q, void* out, unsigned* status, cudaStream_t st)
+{
+    if (n_groups <= 0) return cudaSuccess;
+    const int rows = d.n_q_heads / d.n_kv_heads * group_q;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int nt = nt_for(rows);
+    if (!configure4(dev, nt)) return cudaErrorInvalidValue;
+    int bs_log2 = 0;
+    while ((1 << bs_log2) < d.block_size) ++bs_log2;
+    qsa_attn_plan_info p;
+    plan_kv4(d, n_groups, group_q, &p);
+    const int n_split = p.n_split;
+    const int tiles_max = (kItems4 + kTok4 / d.block_size - 1) / (kTok4 / d.block_size);
+    const int items = (tiles_max + n_split - 1) / n_split * (kTok4 / d.block_size);   // of one split, in whole stages
+    const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / sqrtf((float)d.head_dim);
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = n_split == 1 ? dim3((unsigned)n_groups, (unsigned)d.n_kv_heads, 1u)
+                               : dim3((unsigned)n_split, (unsigned)d.n_kv_heads, (unsigned)n_groups);
+    cfg.blockDim = dim3((unsigned)p.threads);
+    cfg.dynamicSmemBytes = (size_t)p.smem_bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)n_split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = n_split > 1 ? attr : nullptr;
+    cfg.numAttrs = n_split > 1 ? 1 : 0;
+    auto go = [&](auto kern) {
+        return cudaLaunchKernelEx(
+            &cfg, kern, (const uint4*)q, (const uint8_t*)c.k_codes, (const uint8_t*)c.k_scales,
+            (const uint8_t*)c.v_codes, (const uint8_t*)c.v_scales, q_seq, q_pos, sel_idx, sel_cnt, c.page_table,
+            (int)c.page_tokens, c.page_table ? d.kv_capacity / c.page_tokens : (int64_t)0, c.n_pages, (int)d.batch,
+            (int)d.n_q_heads, (int)d.n_kv_heads, d.kv_capacity, bs_log2, (int)d.top_k, group_q,
+            scale * 1.4426950408889634f, items, n_split, (int)p.n_stages, (__nv_bfloat16*)out, status);
+    };
+    return nt == 1 ? go(k_sparse_attn_kv4<1, 2>) : nt == 2 ? go(k_sparse_attn_kv4<2, 2>) : go(k_sparse_attn_kv4<4, 1>);
+}
+
+}  // namespace qsa

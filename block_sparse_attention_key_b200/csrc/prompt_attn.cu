@@ -93,25 +93,6 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
     return d;
 }
 
-// Sequence and tile of grid index x: sequence s's tiles start at cu[s] / TQ + s (TQ tokens
-// per CTA), which leaves every sequence at least ceil(len / TQ) indices and needs no
-// prefix sum.  32-way search by one warp; -1 if x lies before the first sequence.
-__device__ __forceinline__ int find_sequence(const int32_t* __restrict__ cu, int batch, int64_t x, int tq, int lane)
-{
-    int lo = 0, hi = batch;
-    while (hi - lo > 1 || lo == 0) {
-        const int step = (hi - lo + 31) / 32;
-        const int s = lo + lane * step;
-        const bool at = s < hi && (int64_t)(__ldg(cu + s) / tq) + s <= x;
-        const int n = __popc(__ballot_sync(0xffffffffu, at));
-        if (n == 0) return lo == 0 ? -1 : lo;
-        lo += (n - 1) * step;
-        hi = min(lo + step, hi);
-        if (step == 1) break;
-    }
-    return lo;
-}
-
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -130,7 +111,9 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     const int64_t x = n_tiles - 1 - blockIdx.x / n_kv_heads;   // the longest rows of each sequence first
 
     if (warp == 0) {
-        const int s = find_sequence(cu_len, batch, x, tq, lane);
+        // sequence s's tiles start at index cu[s] / tq + s, which leaves every sequence at least
+        // ceil(len / tq) indices and needs no prefix sum
+        const int s = find_sequence(batch, lane, [&](int i) { return (int64_t)(__ldg(cu_len + i) / tq) + i <= x; });
         if (lane == 0) {
             int t0 = 0, len = 0, tok0 = 0;
             if (s >= 0) {

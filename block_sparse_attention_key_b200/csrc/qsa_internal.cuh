@@ -92,6 +92,24 @@ inline cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, siz
 __device__ __forceinline__ float bf16lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t x) { return __uint_as_float(x & 0xFFFF0000u); }
 
+// The sequence of an index in a packed array, by one warp: the largest s in [0, batch) for
+// which below(s) holds (32-way search; below must not become true again after false), -1
+// if there is none.  Bounded and in range for any below.
+template <typename Below>
+__device__ __forceinline__ int find_sequence(int batch, int lane, Below below)
+{
+    int lo = 0, hi = batch;
+    for (bool first = true; first || hi - lo > 1; first = false) {
+        const int step = (hi - lo + 31) / 32;
+        const int s = lo + lane * step;
+        const int n = __popc(__ballot_sync(0xffffffffu, s < hi && below(s)));
+        if (n == 0) return first ? -1 : lo;
+        lo += (n - 1) * step;
+        hi = min(lo + step, hi);
+    }
+    return lo;
+}
+
 // ---- workspace layout ----
 struct WsLayout {
     size_t status = 0;     // u32 status word (first 256 bytes)
@@ -202,6 +220,15 @@ int64_t prompt_attn_ctas(const qsa_dims& d, int32_t n_tok);
 cudaError_t launch_prompt_attn(const qsa_dims& d, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
                                const void* v, int64_t v_ld, const int32_t* cu_len, int32_t n_tok, void* out,
                                unsigned* status, cudaStream_t st);
+
+// 4-bit caches: the append (kv4.cu) and the gathered attention (attn_kv4.cu).
+cudaError_t launch_kv4_append(const qsa_dims& d, const qsa_kv4_cache& c, const void* k, int64_t k_ld, const void* v,
+                              int64_t v_ld, const int32_t* cu_len, const int32_t* len_before, int32_t n_tok,
+                              unsigned* status, cudaStream_t st);
+void plan_kv4(const qsa_dims& d, int64_t n_groups, int group_q, qsa_attn_plan_info* p);  // launch shape
+cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, const void* q, const int32_t* q_seq,
+                                   const int32_t* q_pos, const int32_t* sel_idx, const int32_t* sel_cnt,
+                                   int64_t n_groups, int group_q, void* out, unsigned* status, cudaStream_t st);
 
 // Context-parallel steps (cp.cu).
 size_t cp_partial_row_floats();

@@ -38,7 +38,8 @@ EXPORTED = (
     "qsa_pool_block_keys", "qsa_index_scores", "qsa_topk_blocks", "qsa_sparse_attn", "qsa_forward",
     "qsa_sparse_attn_noalloc", "qsa_sparse_attn_ex", "qsa_select_blocks",
     "qsa_cp_workspace_bytes", "qsa_cp_select_keys", "qsa_cp_merge_keys", "qsa_cp_attn_partial", "qsa_cp_combine",
-    "qsa_attn_plan", "qsa_prompt_attn",
+    "qsa_attn_plan", "qsa_prompt_attn", "qsa_kv4_append", "qsa_sparse_attn_kv4",
+    "qsa_attn_kv4_plan",
 )
 
 CP_PART_ROW = 132  # floats per (query, head) partial of a context shard
@@ -98,6 +99,14 @@ class qsa_prompt_args(ctypes.Structure):
     ]
 
 
+class qsa_kv4_cache(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("page_tokens", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+    ]
+
+
 _lib = None
 
 
@@ -133,6 +142,10 @@ def load(path=LIB_PATH):
     L.qsa_cp_combine.argtypes = [D, I32, P, I32, P, P]
     L.qsa_attn_plan.argtypes = [D, I32, I32, ctypes.POINTER(qsa_attn_plan_info)]
     L.qsa_prompt_attn.argtypes = [D, ctypes.POINTER(qsa_prompt_args), P, P]
+    C = ctypes.POINTER(qsa_kv4_cache)
+    L.qsa_kv4_append.argtypes = [D, C, P, I64, P, I64, P, P, I32, P, P]
+    L.qsa_attn_kv4_plan.argtypes = [D, I32, I32, ctypes.POINTER(qsa_attn_plan_info)]
+    L.qsa_sparse_attn_kv4.argtypes = [D, C, ctypes.POINTER(qsa_attn_args), P, P]
     for name in EXPORTED:
         if name not in ("qsa_workspace_bytes", "qsa_status_string", "qsa_cp_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
@@ -303,6 +316,87 @@ def qsa_prompt_attn(dims, q, k, v, cu_len, n_tok, out, workspace=None, stream=No
     args = qsa_prompt_args(qp, kp, vp, q_ld, k_ld, v_ld, _ptr(cu_len), n_tok, _ptr(out))
     _check("qsa_prompt_attn", load().qsa_prompt_attn(ctypes.byref(dims), ctypes.byref(args), _ptr(workspace),
                                                      _stream(stream)))
+
+
+# ---------------------------------------------------------------- caches in 4 bits
+
+def kv4_cache(k_codes, k_scales, v_codes, v_scales, page_table=None, page_tokens=0, n_pages=0):
+    """The handle of a 4-bit cache: u8 codes [..., 64] and scales [..., 8] over the leading sizes
+    [batch][n_kv_heads][kv_capacity], or [n_pages][n_kv_heads][page_tokens] with a page table
+    (i32 [batch][kv_capacity / page_tokens]).  It keeps the tensors alive; make it once."""
+    import torch
+    lead = tuple(k_codes.shape[:-1])
+    if len(lead) != 3:
+        raise ValueError("codes: [batch or pages][n_kv_heads][tokens][64] expected")
+    for name, t, n in (("k_codes", k_codes, 64), ("v_codes", v_codes, 64), ("k_scales", k_scales, 8),
+                       ("v_scales", v_scales, 8)):
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn if n == 8 else torch.uint8) or tuple(t.shape) != (*lead, n):
+            raise ValueError(f"{name}: u8 {(*lead, n)} expected, got {t.dtype} {tuple(t.shape)}")
+    if page_table is not None:
+        if page_table.dtype != torch.int32 or page_table.dim() != 2:
+            raise ValueError("page_table: i32 [batch][kv_capacity / page_tokens] expected")
+        if lead[0] != n_pages or lead[2] != page_tokens:
+            raise ValueError(f"pools of {n_pages} pages of {page_tokens} tokens expected, got {lead}")
+    cache = qsa_kv4_cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(page_table), page_tokens,
+                          n_pages)
+    cache.lead = lead
+    cache.table_shape = None if page_table is None else tuple(page_table.shape)
+    cache.tensors = (k_codes, k_scales, v_codes, v_scales, page_table)
+    return cache
+
+
+def _fits(dims, cache):
+    """The cache's sizes are the ones dims give (the C ABI cannot see them)."""
+    if cache.table_shape is None:
+        want, got = (dims.batch, dims.n_kv_heads, dims.kv_capacity), cache.lead
+    else:
+        want = (dims.batch, dims.kv_capacity // cache.page_tokens, dims.n_kv_heads)
+        got = (*cache.table_shape, cache.lead[1])
+    if want != got:
+        raise ValueError(f"cache of sizes {got}, but dims give {want}")
+
+
+def qsa_kv4_append(dims, cache, k, v, cu_len, len_before, n_tok, workspace=None, stream=None):
+    """Round packed K/V rows (bf16 [n_tok][n_kv_heads][128], also slices of a projection) to 4 bits
+    into `cache` (kv4_cache): tokens [cu_len[s], cu_len[s+1]) at len_before[s] on."""
+    import torch
+    for name, t in (("k", k), ("v", v)):
+        _like(name, t, torch.bfloat16, (n_tok, dims.n_kv_heads, 128))
+    _like("cu_len", cu_len, torch.int32, (dims.batch + 1,))
+    _like("len_before", len_before, torch.int32, (dims.batch,))
+    _fits(dims, cache)
+    kp, k_ld = _token_rows("k", k, n_tok, dims.n_kv_heads)
+    vp, v_ld = _token_rows("v", v, n_tok, dims.n_kv_heads)
+    _here(cache.tensors[0], k, v, cu_len, len_before, workspace)
+    _check("qsa_kv4_append", load().qsa_kv4_append(
+        ctypes.byref(dims), ctypes.byref(cache), kp, k_ld, vp, v_ld, _ptr(cu_len), _ptr(len_before), n_tok,
+        _ptr(workspace), _stream(stream)))
+
+
+def qsa_attn_kv4_plan(dims, n_q, group_q=1):
+    """qsa_sparse_attn_kv4's launch for n_q queries in groups of group_q (see qsa_attn_plan)."""
+    info = qsa_attn_plan_info()
+    _check("qsa_attn_kv4_plan", load().qsa_attn_kv4_plan(ctypes.byref(dims), n_q, group_q, ctypes.byref(info)))
+    return {name: getattr(info, name) for name, _ in qsa_attn_plan_info._fields_}
+
+
+def qsa_sparse_attn_kv4(dims, cache, q, q_seq, q_pos, sel_idx, sel_cnt, n_q, out, workspace=None, group_q=1,
+                        stream=None):
+    """qsa_sparse_attn_ex over a 4-bit cache (kv4_cache); needs no workspace but for its status."""
+    import torch
+    _fits(dims, cache)
+    groups = n_q // max(group_q, 1)
+    for name, t, dtype, shape in (("q", q, torch.bfloat16, (n_q, dims.n_q_heads, 128)),
+                                  ("out", out, torch.bfloat16, (n_q, dims.n_q_heads, 128)),
+                                  ("q_seq", q_seq, torch.int32, (n_q,)), ("q_pos", q_pos, torch.int32, (n_q,)),
+                                  ("sel_idx", sel_idx, torch.int32, (groups, QSA_SEL_CAP)),
+                                  ("sel_cnt", sel_cnt, torch.int32, (groups,))):
+        _like(name, t, dtype, shape)
+    _here(cache.tensors[0], q, q_seq, q_pos, sel_idx, sel_cnt, out, workspace)
+    args = qsa_attn_args(_ptr(q), None, None, _ptr(q_seq), _ptr(q_pos), _ptr(sel_idx), _ptr(sel_cnt), n_q, group_q,
+                         None, 0, 0, _ptr(out))
+    _check("qsa_sparse_attn_kv4", load().qsa_sparse_attn_kv4(
+        ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(args), _ptr(workspace), _stream(stream)))
 
 
 # ---------------------------------------------------------------- context parallelism (see include/qsa.h)

@@ -306,6 +306,53 @@ typedef struct qsa_forward_args {
 int qsa_forward(const qsa_dims* dims, const qsa_forward_args* args, void* workspace,
                 size_t ws_bytes, void* stream);
 
+/* ---- K/V caches in 4 bits ----
+ *
+ * A row of 128 values (one token, one KV head) is 64 bytes of e2m1 codes (value 2i in the
+ * low half of byte i, 2i + 1 in the high half) and 8 e4m3 scales, one per 16 values:
+ *     value[d] = e2m1(code[d]) * e4m3(scale[d / 16])
+ * (72 bytes instead of 256).  Codes and scales are separate arrays, each laid out like the
+ * bf16 caches with 64 or 8 bytes in the place of the 128 values: [batch][n_kv_heads]
+ * [kv_capacity][64 | 8], or with page_table != NULL pools [n_pages][n_kv_heads]
+ * [page_tokens][64 | 8] (see qsa_sparse_attn_ex).  All pointers 16-byte aligned.  The
+ * indexer's keys and the pooled cache stay as they are. */
+typedef struct qsa_kv4_cache {
+    void* k_codes;              /* u8 */
+    void* k_scales;             /* e4m3 */
+    void* v_codes;
+    void* v_scales;
+    const int32_t* page_table;  /* NULL: dense caches */
+    int32_t page_tokens;        /* tokens per page (paged only) */
+    int64_t n_pages;            /* pages in each pool (paged only) */
+} qsa_kv4_cache;
+
+/* Append: the packed tokens [cu_len[s], cu_len[s+1]) of sequence s go to positions
+ * len_before[s], len_before[s] + 1, ... of its cache (cu_len i32 [batch + 1], len_before
+ * i32 [batch], on the device).  For each 16 values x: scale = e4m3(max|x| / 6), at least
+ * 2^-9 and at most 448, code = e2m1(x / scale), both round to nearest even, larger
+ * magnitudes saturating; 16 values with one that is not finite get the scale NaN (0x7F)
+ * and codes 0, so they read as NaN.
+ * k, v: bf16, head h of token i at element i * ld + h * head_dim (ld a multiple of 8, at
+ * least n_kv_heads * head_dim).  A sequence whose bounds decrease, leave [0, n_tok] or
+ * would pass kv_capacity is skipped and QSA_DEV_BAD_LEN set; a row whose page entry is
+ * outside [0, n_pages) is skipped and QSA_DEV_BAD_PAGE set.  Pages given to two sequences
+ * must not be appended to (see qsa_pages_update).
+ * workspace: may be NULL (then device errors are not reported). */
+int qsa_kv4_append(const qsa_dims* dims, const qsa_kv4_cache* cache, const void* k, int64_t k_ld, const void* v,
+                   int64_t v_ld, const int32_t* cu_len, const int32_t* len_before, int32_t n_tok, void* workspace,
+                   void* stream);
+
+/* Step 4 over such a cache: qsa_sparse_attn_ex's arguments, rules and result, K and V
+ * being the cache's values (k_cache, v_cache and the page fields of `args` must be NULL
+ * and 0: the cache holds them).  A row that attends nothing is 0.  No scratch: workspace
+ * may be NULL (then device errors are not reported). */
+int qsa_sparse_attn_kv4(const qsa_dims* dims, const qsa_kv4_cache* cache, const qsa_attn_args* args, void* workspace,
+                        void* stream);
+
+/* The launch qsa_sparse_attn_kv4 makes for n_q queries in groups of group_q (host
+ * arithmetic only, see qsa_attn_plan; splits always merge in a cluster). */
+int qsa_attn_kv4_plan(const qsa_dims* dims, int32_t n_q, int32_t group_q, qsa_attn_plan_info* info);
+
 /* ---- whole prompts: dense causal attention, packed ----
  *
  * out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h].k[j][g]) v[j][g], j over the tokens

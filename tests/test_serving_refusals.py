@@ -63,3 +63,94 @@ def test_tensors_of_another_device_are_refused(qsa, monkeypatch):
         qsa._here(None, Far())
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     qsa._here(None, Far())
+
+
+def _cache(qsa, **kw):
+    base = dict(k_codes=16, k_scales=32, v_codes=48, v_scales=64, page_table=None, page_tokens=0, n_pages=0)
+    return qsa.qsa_kv4_cache(**{**base, **kw})
+
+
+def test_kv4_append_refusals(qsa):
+    lib = qsa.load()
+    d = _dims(qsa)
+    good = dict(k=16, k_ld=512, v=16, v_ld=512, cu=16, before=16, n=5)
+
+    def call(dims=d, cache=None, ws=None, **kw):
+        a = {**good, **kw}
+        return lib.qsa_kv4_append(ctypes.byref(dims), ctypes.byref(cache or _cache(qsa)), a["k"], a["k_ld"], a["v"],
+                                  a["v_ld"], a["cu"], a["before"], a["n"], ws, None)
+
+    for kw in (dict(k=None), dict(v=8), dict(cu=None), dict(before=4), dict(n=-1), dict(k_ld=504), dict(v_ld=515), dict(ws=8),
+               dict(cache=_cache(qsa, k_codes=None)), dict(cache=_cache(qsa, v_scales=24)),
+               dict(cache=_cache(qsa, page_table=16, page_tokens=6, n_pages=4)),
+               dict(cache=_cache(qsa, page_table=16, page_tokens=16, n_pages=0)),
+               dict(cache=_cache(qsa, page_table=16, page_tokens=4096 * 2, n_pages=4))):
+        assert call(**kw) == qsa.QSA_ERR_INVALID_ARG, kw
+    assert lib.qsa_kv4_append(ctypes.byref(d), None, 16, 512, 16, 512, 16, 16, 1, None, None) == qsa.QSA_ERR_INVALID_ARG
+    assert call(dims=_dims(qsa, n_q_heads=1 << 20, n_kv_heads=1 << 20), k_ld=1 << 27, v_ld=1 << 27,
+                n=1 << 20) == qsa.QSA_ERR_UNSUPPORTED
+    assert call(n=0, k=None) == qsa.QSA_OK
+
+
+def test_kv4_attention_refusals(qsa):
+    lib = qsa.load()
+    d = _dims(qsa)
+    good = dict(q=16, q_seq=16, q_pos=16, sel_idx=16, sel_cnt=16, n_q=4, group_q=1, out=16)
+
+    def call(dims=d, cache=None, ws=None, **kw):
+        a = qsa.qsa_attn_args(**{**good, **kw})
+        return lib.qsa_sparse_attn_kv4(ctypes.byref(dims), ctypes.byref(cache or _cache(qsa)), ctypes.byref(a), ws, None)
+
+    for kw in (dict(q=None), dict(q_seq=4), dict(q_pos=None), dict(sel_idx=8), dict(sel_cnt=None), dict(out=None),
+               dict(n_q=-1), dict(group_q=0), dict(group_q=3), dict(k_cache=16), dict(v_cache=16), dict(page_table=16),
+               dict(page_tokens=16), dict(n_pages=1), dict(ws=24), dict(cache=_cache(qsa, k_scales=None)),
+               dict(cache=_cache(qsa, page_table=16, page_tokens=16, n_pages=-1))):
+        assert call(**kw) == qsa.QSA_ERR_INVALID_ARG, kw
+    assert lib.qsa_sparse_attn_kv4(ctypes.byref(d), ctypes.byref(_cache(qsa)), None, None, None) == qsa.QSA_ERR_INVALID_ARG
+    for kw in (dict(n_q=65536), dict(n_q=8, group_q=8), dict(dims=_dims(qsa, n_q_heads=65536, n_kv_heads=65536))):
+        assert call(**kw) == qsa.QSA_ERR_UNSUPPORTED, kw
+    assert call(n_q=0, q=None) == qsa.QSA_OK
+
+
+def test_kv4_binding_checks_the_cache(qsa, monkeypatch):
+    monkeypatch.setattr(qsa, "_ptr", lambda t: None if t is None else 16)
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    c = qsa.kv4_cache(u8(4, 2, 64, 64), u8(4, 2, 64, 8), u8(4, 2, 64, 64), u8(4, 2, 64, 8))
+    qsa._fits(_dims(qsa, n_q_heads=4, n_kv_heads=2, kv_capacity=64), c)
+    for kw in (dict(batch=5), dict(n_kv_heads=1), dict(kv_capacity=128)):
+        with pytest.raises(ValueError, match="dims give"):
+            qsa._fits(_dims(qsa, **{**dict(n_q_heads=4, n_kv_heads=2, kv_capacity=64), **kw}), c)
+    table = torch.zeros((4, 4), dtype=torch.int32)
+    pages = (u8(9, 2, 16, 64), u8(9, 2, 16, 8), u8(9, 2, 16, 64), u8(9, 2, 16, 8))
+    p = qsa.kv4_cache(*pages, table, 16, 9)
+    qsa._fits(_dims(qsa, n_q_heads=4, n_kv_heads=2, kv_capacity=64), p)
+    with pytest.raises(ValueError, match="dims give"):
+        qsa._fits(_dims(qsa, n_q_heads=4, n_kv_heads=2, kv_capacity=80), p)
+    for bad in ((pages[0], pages[1], pages[2], pages[1][:4], table, 16, 9), (pages[0].int(), *pages[1:], table, 16, 9),
+                (*pages, table.long(), 16, 9), (*pages, table, 16, 8), (*pages, table, 32, 9)):
+        with pytest.raises(ValueError):
+            qsa.kv4_cache(*bad)
+
+
+def test_kv4_plans_fit_the_hardware(qsa):
+    """Launch shapes of the 4-bit attention: every tile of the longest list has a split, no split is
+    empty, merge buffers and stages fit 227 KB (an independent restatement of the layout)."""
+    import itertools
+    import math
+    for rows, bs, pairs in itertools.product((1, 8, 9, 16, 17, 32), (1, 2, 4, 8, 16), (1, 2, 3, 7, 9, 16, 37, 64, 100, 147, 148, 5000)):
+        rp = 8 if rows <= 8 else 16 if rows <= 16 else 32
+        d = qsa.make_dims(1, rows, 1, 65536, block_size=bs)
+        info = qsa.qsa_attn_plan_info()
+        assert qsa.load().qsa_attn_kv4_plan(ctypes.byref(d), pairs, 1, ctypes.byref(info)) == qsa.QSA_OK
+        per_stage = 64 // bs
+        tiles = math.ceil(514 / per_stage)
+        assert 1 <= info.n_split <= 16 and info.rows == rows and info.ctas == pairs * info.n_split
+        assert info.n_split == 1 or info.ctas <= 148
+        assert 1 <= info.n_stages <= 16
+        own = math.ceil(tiles / info.n_split)
+        assert (info.n_split - 1) * own < tiles            # the last split has a tile
+        assert own * per_stage <= 592                      # items of a split fit their list
+        warps = info.threads // 32
+        assert max(info.n_split, warps) * rp * 130 * 4 <= info.n_stages * 9216
+        assert info.smem_bytes >= rp * 256 + info.n_stages * (9216 + 256) + 592 * 12 + 256
+        assert info.smem_bytes + 1024 <= 227 * 1024
