@@ -11,5 +11,5 @@ from .qsa import (  # noqa: F401
     qsa_sparse_attn_ex, qsa_select_blocks, QSA_DEV_BAD_PAGE, QSA_SEL_CAP, CP_PART_ROW,
     qsa_cp_workspace_bytes, qsa_cp_select_keys, qsa_cp_merge_keys, qsa_cp_attn_partial, qsa_cp_combine,
     qsa_attn_plan, qsa_prompt_attn, kv4_cache, qsa_kv4_append, qsa_sparse_attn_kv4,
-    qsa_attn_kv4_plan,
+    qsa_attn_kv4_plan, page_pools, qsa_pages_workspace_bytes, qsa_pages_update, qsa_pages_compact, QSA_MAX_POOLS,
 )

@@ -547,6 +547,64 @@ int qsa_attn_kv4_plan(const qsa_dims* dims, int32_t n_q, int32_t group_q, qsa_at
     return QSA_OK;
 }
 
+// ---------------------------------------------------------------- pages
+
+static int check_page_sizes(const qsa_dims* d, int32_t page_tokens, int64_t n_pages)
+{
+    if (page_tokens < 1 || page_tokens % d->block_size != 0 || d->kv_capacity % page_tokens != 0 || n_pages < 1 ||
+        n_pages > (1ll << 31) - 1)
+        return QSA_ERR_INVALID_ARG;
+    // scans run in strides of 8,192 pages, ranks over the whole table in 32 bits
+    return n_pages > (1ll << 30) || d->batch * (d->kv_capacity / page_tokens) > INT32_MAX ? QSA_ERR_UNSUPPORTED : QSA_OK;
+}
+
+static int check_pools(const qsa_dims* d, const qsa_page_pools* p, const int32_t* page_table, const int32_t* page_ref,
+                       const void* workspace, size_t ws_bytes)
+{
+    if (!p || p->n_pools < 0 || p->n_pools > QSA_MAX_POOLS) return QSA_ERR_INVALID_ARG;
+    const int rc = check_page_sizes(d, p->page_tokens, p->n_pages);
+    if (rc != QSA_OK) return rc;
+    for (int i = 0; i < p->n_pools; ++i) {
+        if (!aligned16(p->pool[i]) || p->page_bytes[i] < 16 || p->page_bytes[i] % 16 != 0) return QSA_ERR_INVALID_ARG;
+        if (p->page_bytes[i] > (1ll << 31)) return QSA_ERR_UNSUPPORTED;
+    }
+    if (!aligned16(page_table) || !aligned16(page_ref) || !aligned16(workspace)) return QSA_ERR_INVALID_ARG;
+    return ws_bytes < pages_workspace_bytes(*d, p->n_pages) ? QSA_ERR_WORKSPACE_TOO_SMALL : QSA_OK;
+}
+
+size_t qsa_pages_workspace_bytes(const qsa_dims* dims, int32_t page_tokens, int64_t n_pages)
+{
+    if (check_dims(dims) != QSA_OK || check_page_sizes(dims, page_tokens, n_pages) != QSA_OK) return 0;
+    return pages_workspace_bytes(*dims, n_pages);
+}
+
+int qsa_pages_update(const qsa_dims* dims, const qsa_page_pools* pools, int32_t* page_table, int32_t* page_ref,
+                     const int32_t* free_seq, int32_t n_free, const int32_t* fork_src, const int32_t* fork_dst,
+                     int32_t n_fork, const int32_t* len_before, const int32_t* len_after, void* workspace,
+                     size_t ws_bytes, void* stream)
+{
+    int rc = check_dims(dims);
+    if (rc != QSA_OK) return rc;
+    if (n_free < 0 || n_fork < 0) return QSA_ERR_INVALID_ARG;
+    if ((n_free > 0 && !aligned16(free_seq)) || (n_fork > 0 && (!aligned16(fork_src) || !aligned16(fork_dst))) ||
+        !aligned16(len_before) || !aligned16(len_after))
+        return QSA_ERR_INVALID_ARG;
+    if ((rc = check_pools(dims, pools, page_table, page_ref, workspace, ws_bytes)) != QSA_OK) return rc;
+    return cuda_status(launch_pages_update(*dims, *pools, page_table, page_ref, free_seq, n_free, fork_src, fork_dst,
+                                           n_fork, len_before, len_after, (char*)workspace, (cudaStream_t)stream));
+}
+
+int qsa_pages_compact(const qsa_dims* dims, const qsa_page_pools* pools, int32_t* page_table, int32_t* page_ref,
+                      int32_t* n_live, void* workspace, size_t ws_bytes, void* stream)
+{
+    int rc = check_dims(dims);
+    if (rc != QSA_OK) return rc;
+    if (!aligned16(n_live)) return QSA_ERR_INVALID_ARG;
+    if ((rc = check_pools(dims, pools, page_table, page_ref, workspace, ws_bytes)) != QSA_OK) return rc;
+    return cuda_status(launch_pages_compact(*dims, *pools, page_table, page_ref, n_live, (char*)workspace,
+                                            (cudaStream_t)stream));
+}
+
 // ---------------------------------------------------------------- whole prompts
 
 int qsa_prompt_attn(const qsa_dims* dims, const qsa_prompt_args* a, void* workspace, void* stream)

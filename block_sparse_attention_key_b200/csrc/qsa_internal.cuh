@@ -230,6 +230,15 @@ cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, co
                                    const int32_t* q_pos, const int32_t* sel_idx, const int32_t* sel_cnt,
                                    int64_t n_groups, int group_q, void* out, unsigned* status, cudaStream_t st);
 
+// Page bookkeeping (pages.cu); ws: a workspace of at least pages_workspace_bytes.
+size_t pages_workspace_bytes(const qsa_dims& d, int64_t n_pages);
+cudaError_t launch_pages_update(const qsa_dims& d, const qsa_page_pools& p, int32_t* page_table, int32_t* page_ref,
+                                const int32_t* free_seq, int32_t n_free, const int32_t* fork_src,
+                                const int32_t* fork_dst, int32_t n_fork, const int32_t* len_before,
+                                const int32_t* len_after, char* ws, cudaStream_t st);
+cudaError_t launch_pages_compact(const qsa_dims& d, const qsa_page_pools& p, int32_t* page_table, int32_t* page_ref,
+                                 int32_t* n_live, char* ws, cudaStream_t st);
+
 // Context-parallel steps (cp.cu).
 size_t cp_partial_row_floats();
 cudaError_t launch_cp_local_pos(const int32_t* q_pos, int32_t n_q, int64_t tok_lo, int64_t cap_loc, int32_t* pos_loc,

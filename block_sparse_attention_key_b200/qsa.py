@@ -39,7 +39,7 @@ EXPORTED = (
     "qsa_sparse_attn_noalloc", "qsa_sparse_attn_ex", "qsa_select_blocks",
     "qsa_cp_workspace_bytes", "qsa_cp_select_keys", "qsa_cp_merge_keys", "qsa_cp_attn_partial", "qsa_cp_combine",
     "qsa_attn_plan", "qsa_prompt_attn", "qsa_kv4_append", "qsa_sparse_attn_kv4",
-    "qsa_attn_kv4_plan",
+    "qsa_attn_kv4_plan", "qsa_pages_workspace_bytes", "qsa_pages_update", "qsa_pages_compact",
 )
 
 CP_PART_ROW = 132  # floats per (query, head) partial of a context shard
@@ -107,6 +107,16 @@ class qsa_kv4_cache(ctypes.Structure):
     ]
 
 
+QSA_MAX_POOLS = 128
+
+
+class qsa_page_pools(ctypes.Structure):
+    _fields_ = [
+        ("n_pools", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("n_pages", ctypes.c_int64),
+        ("pool", ctypes.c_void_p * QSA_MAX_POOLS), ("page_bytes", ctypes.c_int64 * QSA_MAX_POOLS),
+    ]
+
+
 _lib = None
 
 
@@ -146,8 +156,14 @@ def load(path=LIB_PATH):
     L.qsa_kv4_append.argtypes = [D, C, P, I64, P, I64, P, P, I32, P, P]
     L.qsa_attn_kv4_plan.argtypes = [D, I32, I32, ctypes.POINTER(qsa_attn_plan_info)]
     L.qsa_sparse_attn_kv4.argtypes = [D, C, ctypes.POINTER(qsa_attn_args), P, P]
+    PP = ctypes.POINTER(qsa_page_pools)
+    L.qsa_pages_workspace_bytes.argtypes = [D, I32, I64]
+    L.qsa_pages_workspace_bytes.restype = SZ
+    L.qsa_pages_update.argtypes = [D, PP, P, P, P, I32, P, P, I32, P, P, P, SZ, P]
+    L.qsa_pages_compact.argtypes = [D, PP, P, P, P, P, SZ, P]
     for name in EXPORTED:
-        if name not in ("qsa_workspace_bytes", "qsa_status_string", "qsa_cp_workspace_bytes"):
+        if name not in ("qsa_workspace_bytes", "qsa_status_string", "qsa_cp_workspace_bytes",
+                        "qsa_pages_workspace_bytes"):
             getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -397,6 +413,61 @@ def qsa_sparse_attn_kv4(dims, cache, q, q_seq, q_pos, sel_idx, sel_cnt, n_q, out
                          None, 0, 0, _ptr(out))
     _check("qsa_sparse_attn_kv4", load().qsa_sparse_attn_kv4(
         ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(args), _ptr(workspace), _stream(stream)))
+
+
+# ---------------------------------------------------------------- pages of a paged cache
+
+def page_pools(pools, page_tokens, n_pages):
+    """The handle of the pools that share one page table: tensors whose first size is n_pages, of any
+    type (K and V, or codes and scales, of every layer).  It keeps them alive; make it once."""
+    if len(pools) > QSA_MAX_POOLS:
+        raise ValueError(f"at most {QSA_MAX_POOLS} pools")
+    p = qsa_page_pools(len(pools), page_tokens, n_pages)
+    for i, t in enumerate(pools):
+        if t.shape[0] != n_pages:
+            raise ValueError(f"pool {i}: {n_pages} pages expected, got {tuple(t.shape)}")
+        p.pool[i] = _ptr(t)
+        p.page_bytes[i] = t.numel() // n_pages * t.element_size()
+    p.tensors = tuple(pools)
+    return p
+
+
+def qsa_pages_workspace_bytes(dims, page_tokens, n_pages):
+    return int(load().qsa_pages_workspace_bytes(ctypes.byref(dims), page_tokens, n_pages))
+
+
+def _page_state(dims, pools, page_table, page_ref, *more):
+    import torch
+    _like("page_table", page_table, torch.int32, (dims.batch, dims.kv_capacity // pools.page_tokens))
+    _like("page_ref", page_ref, torch.int32, (pools.n_pages,))
+    _here(page_table, page_ref, *pools.tensors[:1], *more)
+
+
+def qsa_pages_update(dims, pools, page_table, page_ref, len_before, len_after, workspace, free_seq=None, n_free=0,
+                     fork_src=None, fork_dst=None, n_fork=0, stream=None):
+    """A scheduler's step on a paged cache (page_pools): free sequences, fork others, then make every
+    page of positions [len_before, len_after) the sequence's own, copying what was shared."""
+    import torch
+    for name, t, n in (("free_seq", free_seq, n_free), ("fork_src", fork_src, n_fork), ("fork_dst", fork_dst, n_fork)):
+        if n > 0 and (t is None or t.dtype != torch.int32 or t.numel() < n):
+            raise ValueError(f"{name}: {n} int32 values expected")
+    _like("len_before", len_before, torch.int32, (dims.batch,))
+    _like("len_after", len_after, torch.int32, (dims.batch,))
+    _page_state(dims, pools, page_table, page_ref, len_before, len_after, workspace, free_seq, fork_src, fork_dst)
+    _check("qsa_pages_update", load().qsa_pages_update(
+        ctypes.byref(dims), ctypes.byref(pools), _ptr(page_table), _ptr(page_ref), _ptr(free_seq) if n_free else None,
+        n_free, _ptr(fork_src) if n_fork else None, _ptr(fork_dst) if n_fork else None, n_fork, _ptr(len_before),
+        _ptr(len_after), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def qsa_pages_compact(dims, pools, page_table, page_ref, n_live, workspace, stream=None):
+    """Move the live pages of every pool to the ids [0, n_live) (n_live: i32 [1], written)."""
+    import torch
+    _like("n_live", n_live, torch.int32, (1,))
+    _page_state(dims, pools, page_table, page_ref, n_live, workspace)
+    _check("qsa_pages_compact", load().qsa_pages_compact(
+        ctypes.byref(dims), ctypes.byref(pools), _ptr(page_table), _ptr(page_ref), _ptr(n_live), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 # ---------------------------------------------------------------- context parallelism (see include/qsa.h)

@@ -353,6 +353,59 @@ int qsa_sparse_attn_kv4(const qsa_dims* dims, const qsa_kv4_cache* cache, const 
  * arithmetic only, see qsa_attn_plan; splits always merge in a cluster). */
 int qsa_attn_kv4_plan(const qsa_dims* dims, int32_t n_q, int32_t group_q, qsa_attn_plan_info* info);
 
+/* ---- pages of a paged cache ----
+ *
+ * page_table i32 [batch][kv_capacity / page_tokens]: the page of each stretch of
+ * page_tokens tokens, -1 for none.  page_ref i32 [n_pages]: how many table entries name
+ * the page, 0 for a free one.  The caller starts with a table of -1 and counts of 0; the
+ * two calls below keep them consistent.  Sequences forked from one another share pages
+ * until one of them appends.  One table serves every layer and array that is paged alike:
+ * `pools` names them all (K and V, or codes and scales, of each layer), page p of pool i
+ * being bytes [p * page_bytes[i], (p + 1) * page_bytes[i]) (page_bytes a multiple of 16). */
+#define QSA_MAX_POOLS 128
+
+typedef struct qsa_page_pools {
+    int32_t n_pools;      /* 0 .. QSA_MAX_POOLS */
+    int32_t page_tokens;  /* as in qsa_sparse_attn_ex */
+    int64_t n_pages;      /* pages in each pool */
+    void* pool[QSA_MAX_POOLS];
+    int64_t page_bytes[QSA_MAX_POOLS];
+} qsa_page_pools;
+
+/* Workspace bytes of the two calls (0 on invalid arguments); initialise it with
+ * qsa_workspace_init.  A larger workspace of another call serves as well. */
+size_t qsa_pages_workspace_bytes(const qsa_dims* dims, int32_t page_tokens, int64_t n_pages);
+
+/* A scheduler's step, before the appends of the next model step.  In this order:
+ *   free     the sequences free_seq[0 .. n_free) give all their pages back (a page returns
+ *            to the free ones when its last holder gives it back);
+ *   fork     fork_dst[i] gets every page of fork_src[i] (i < n_fork), shared.  A target
+ *            must hold no page and be nobody's source in the list; of forks with one
+ *            target the first counts;
+ *   reserve  every page that positions [len_before[s], len_after[s]) of a sequence touch
+ *            (i32 [batch]; equal lengths: none) becomes its own: a missing page is taken
+ *            from the free ones, a shared one is replaced by one, with its contents copied
+ *            in every pool where it holds tokens below len_before[s].  Free pages are
+ *            taken lowest first, in the order of (sequence, position).  Sharing is judged
+ *            as it stands before this phase: a page that all its holders leave at once
+ *            becomes free for the next call.
+ * Rows of the indexer's keys and the pooled cache are not paged; a fork's are copied by
+ * the caller.  Device status: QSA_DEV_BAD_SEQ (a free or fork that names no sequence, or
+ * a fork that breaks the rules above: skipped), QSA_DEV_BAD_LEN (lengths outside
+ * [0, kv_capacity] or decreasing: nothing reserved), QSA_DEV_BAD_PAGE (an entry past
+ * n_pages, taken for -1, or not enough free pages: the places left over keep their
+ * entries, and the call may be repeated with n_free = n_fork = 0 once there are some). */
+int qsa_pages_update(const qsa_dims* dims, const qsa_page_pools* pools, int32_t* page_table, int32_t* page_ref,
+                     const int32_t* free_seq, int32_t n_free, const int32_t* fork_src, const int32_t* fork_dst,
+                     int32_t n_fork, const int32_t* len_before, const int32_t* len_after, void* workspace,
+                     size_t ws_bytes, void* stream);
+
+/* Moves the live pages to the ids [0, n_live): the k-th free id below n_live takes the
+ * k-th live id from n_live on (contents in every pool, count, table entries), the others
+ * stay.  *n_live: device i32.  The memory from page n_live on holds nothing any more. */
+int qsa_pages_compact(const qsa_dims* dims, const qsa_page_pools* pools, int32_t* page_table, int32_t* page_ref,
+                      int32_t* n_live, void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- whole prompts: dense causal attention, packed ----
  *
  * out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h].k[j][g]) v[j][g], j over the tokens

@@ -154,3 +154,64 @@ def test_kv4_plans_fit_the_hardware(qsa):
         assert max(info.n_split, warps) * rp * 130 * 4 <= info.n_stages * 9216
         assert info.smem_bytes >= rp * 256 + info.n_stages * (9216 + 256) + 592 * 12 + 256
         assert info.smem_bytes + 1024 <= 227 * 1024
+
+
+def test_pages_refusals(qsa):
+    lib = qsa.load()
+    d = _dims(qsa)
+
+    def pools(n=1, pool=16, size=64, page_tokens=16, n_pages=100):
+        p = qsa.qsa_page_pools(n, page_tokens, n_pages)
+        p.pool[0], p.page_bytes[0] = pool, size
+        return p
+
+    need = qsa.qsa_pages_workspace_bytes(d, 16, 100)
+    assert need > 0
+    good = dict(table=16, ref=16, free=16, n_free=1, src=16, dst=16, n_fork=1, before=16, after=16, ws=16, n=need, live=16)
+
+    def update(dims=d, p=None, **kw):
+        a = {**good, **kw}
+        return lib.qsa_pages_update(ctypes.byref(dims), ctypes.byref(p or pools()), a["table"], a["ref"], a["free"],
+                                    a["n_free"], a["src"], a["dst"], a["n_fork"], a["before"], a["after"], a["ws"],
+                                    a["n"], None)
+
+    def compact(dims=d, p=None, **kw):
+        a = {**good, **kw}
+        return lib.qsa_pages_compact(ctypes.byref(dims), ctypes.byref(p or pools()), a["table"], a["ref"], a["live"],
+                                     a["ws"], a["n"], None)
+
+    both = (dict(table=None), dict(ref=8), dict(ws=None), dict(p=pools(n=-1)), dict(p=pools(n=129)), dict(p=pools(pool=None)),
+            dict(p=pools(pool=8)), dict(p=pools(size=0)), dict(p=pools(size=40)), dict(p=pools(page_tokens=6)),
+            dict(p=pools(page_tokens=0)), dict(p=pools(n_pages=0)), dict(dims=_dims(qsa, batch=0)))
+    for kw in both:
+        assert update(**kw) == compact(**kw) == qsa.QSA_ERR_INVALID_ARG, kw
+    for kw in (dict(n_free=-1), dict(n_fork=-1), dict(free=None), dict(src=None), dict(dst=4), dict(before=None), dict(after=8)):
+        assert update(**kw) == qsa.QSA_ERR_INVALID_ARG, kw
+    assert compact(live=None) == qsa.QSA_ERR_INVALID_ARG
+    assert update(n=need - 1) == compact(n=need - 1) == qsa.QSA_ERR_WORKSPACE_TOO_SMALL
+    for kw in (dict(p=pools(n_pages=(1 << 30) + 1)), dict(p=pools(size=(1 << 31) + 16)),
+               dict(dims=_dims(qsa, batch=65535, kv_capacity=1 << 20))):
+        assert update(**kw) == compact(**kw) == qsa.QSA_ERR_UNSUPPORTED, kw
+    for bad in ((d, 16, 0), (d, 5, 10), (_dims(qsa, top_k=0), 16, 10), (_dims(qsa, batch=65535, kv_capacity=1 << 20), 16, 10)):
+        assert qsa.qsa_pages_workspace_bytes(*bad) == 0
+
+
+def test_pages_binding_checks(qsa, monkeypatch):
+    monkeypatch.setattr(qsa, "_ptr", lambda t: None if t is None else 16)
+    d = _dims(qsa)
+    p = qsa.page_pools([torch.zeros(7, 4, 16, 128, dtype=torch.bfloat16), torch.zeros(7, 4, 16, 8, dtype=torch.uint8)], 16, 7)
+    assert list(p.page_bytes[:2]) == [4 * 16 * 256, 4 * 16 * 8] and p.n_pools == 2
+    with pytest.raises(ValueError, match="pages expected"):
+        qsa.page_pools([torch.zeros(6, 16)], 16, 7)
+    with pytest.raises(ValueError, match="at most"):
+        qsa.page_pools([torch.zeros(7, 16)] * 129, 16, 7)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    table, ref, n4 = i32(4, 256), i32(7), i32(4)
+    for bad in (dict(table=i32(4, 255)), dict(ref=i32(8)), dict(before=i32(5)), dict(after=n4.long()), dict(n_free=1),
+                dict(n_fork=5, src=n4, dst=n4)):
+        a = {**dict(table=table, ref=ref, before=n4, after=n4, n_free=0, src=None, dst=None, n_fork=0), **bad}
+        with pytest.raises(ValueError, match="expected"):
+            qsa.qsa_pages_update(d, p, a["table"], a["ref"], a["before"], a["after"], torch.zeros(16), n_free=a["n_free"],
+                                 fork_src=a["src"], fork_dst=a["dst"], n_fork=a["n_fork"])
+    with pytest.raises(ValueError, match="n_live"):
+        qsa.qsa_pages_compact(d, p, table, ref, i32(2), torch.zeros(16))
