@@ -9,6 +9,8 @@ There is no CPU fallback: if the library or a GPU is missing, calls raise.
 import ctypes
 import os
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqsa.so")
 
@@ -184,6 +186,12 @@ def _check(fn, rc):
         raise QsaError(fn, rc, status_string(rc))
 
 
+# the calls behind torch.cuda.current_device() and current_stream(), without their wrappers' few
+# microseconds (a decode step's kernels take not many more)
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _ptr(t):
     if t is None:
         return None
@@ -199,8 +207,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    return _current_stream(_current_device())
 
 
 # ---------------------------------------------------------------- entry points (same names as the C ABI)
@@ -291,47 +298,66 @@ def qsa_forward(dims, *, q, k_cache, v_cache, idx_k, pooled, q_idx, w, len_befor
                                              workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
-# ---------------------------------------------------------------- whole prompts
+# ---------------------------------------------------------------- checked arguments of the serving operators
 
-def _like(name, t, dtype, shape):
-    """Type and shape of an argument (the C ABI cannot see either)."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
-
-
-def _here(*tensors):
-    """Launches go to the current device: every tensor has to lie there."""
-    import torch
-    dev = torch.cuda.current_device() if any(t is not None and t.is_cuda for t in tensors) else None
-    for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != dev:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
-
-
-def _token_rows(name, t, n_tok, heads):
-    """Pointer and token stride of bf16 [n_tok][heads][128], heads dense, tokens any stride."""
-    if not t.is_cuda:
+def _device_of(t):
+    """Device index of a call's first tensor.  Launches go to the current device, so it has to be that."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("libqsa takes CUDA tensors only (no CPU path)")
-    if n_tok and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != 128)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), t.stride(0) if n_tok > 1 else heads * 128
+    if dev != _current_device():
+        raise ValueError(f"tensor on cuda:{dev}, but the current device is cuda:{_current_device()}")
+    return dev
 
+
+def _arg(name, t, dtype, shape, dev):
+    """Pointer of a dense tensor of this type, shape (the C ABI sees neither) and device."""
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: {dtype} {shape} expected, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor on {t.device}, but the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_arg(name, t, n_tok, heads, dev):
+    """Pointer and token stride of bf16 [n_tok][heads][128], heads dense, tokens at any stride."""
+    if t.dtype is not torch.bfloat16 or t.shape != (n_tok, heads, 128):
+        raise ValueError(f"{name}: torch.bfloat16 {(n_tok, heads, 128)} expected, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensor on {t.device}, but the current device is cuda:{dev}")
+    tok, head, one = t.stride()
+    if n_tok and (one != 1 or (heads > 1 and head != 128)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), tok if n_tok > 1 else heads * 128
+
+
+def _workspace_arg(workspace, dev):
+    """Pointer of an optional workspace."""
+    if workspace is None:
+        return None
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace: tensor on {workspace.device}, but the current device is cuda:{dev}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace: tensors must be contiguous")
+    return workspace.data_ptr()
+
+
+# ---------------------------------------------------------------- whole prompts
 
 def qsa_prompt_attn(dims, q, k, v, cu_len, n_tok, out, workspace=None, stream=None):
     """Causal attention over packed whole prompts.  q, k, v: bf16 [n_tok][heads][128], also as
     slices of a fused projection; cu_len: i32 [batch + 1]; out: bf16 [n_tok][n_q_heads][128]."""
-    import torch
-    for name, t, heads in (("q", q, dims.n_q_heads), ("k", k, dims.n_kv_heads), ("v", v, dims.n_kv_heads),
-                           ("out", out, dims.n_q_heads)):
-        _like(name, t, torch.bfloat16, (n_tok, heads, 128))
-    _like("cu_len", cu_len, torch.int32, (dims.batch + 1,))
-    qp, q_ld = _token_rows("q", q, n_tok, dims.n_q_heads)
-    kp, k_ld = _token_rows("k", k, n_tok, dims.n_kv_heads)
-    vp, v_ld = _token_rows("v", v, n_tok, dims.n_kv_heads)
-    _here(q, k, v, cu_len, out, workspace)
-    args = qsa_prompt_args(qp, kp, vp, q_ld, k_ld, v_ld, _ptr(cu_len), n_tok, _ptr(out))
-    _check("qsa_prompt_attn", load().qsa_prompt_attn(ctypes.byref(dims), ctypes.byref(args), _ptr(workspace),
-                                                     _stream(stream)))
+    dev, hq, hkv = _device_of(q), dims.n_q_heads, dims.n_kv_heads
+    qp, q_ld = _rows_arg("q", q, n_tok, hq, dev)
+    kp, k_ld = _rows_arg("k", k, n_tok, hkv, dev)
+    vp, v_ld = _rows_arg("v", v, n_tok, hkv, dev)
+    args = qsa_prompt_args(qp, kp, vp, q_ld, k_ld, v_ld, _arg("cu_len", cu_len, torch.int32, (dims.batch + 1,), dev),
+                           n_tok, _arg("out", out, torch.bfloat16, (n_tok, hq, 128), dev))
+    rc = load().qsa_prompt_attn(dims, args, _workspace_arg(workspace, dev), _stream(stream))
+    if rc:
+        _check("qsa_prompt_attn", rc)
 
 
 # ---------------------------------------------------------------- caches in 4 bits
@@ -340,53 +366,51 @@ def kv4_cache(k_codes, k_scales, v_codes, v_scales, page_table=None, page_tokens
     """The handle of a 4-bit cache: u8 codes [..., 64] and scales [..., 8] over the leading sizes
     [batch][n_kv_heads][kv_capacity], or [n_pages][n_kv_heads][page_tokens] with a page table
     (i32 [batch][kv_capacity / page_tokens]).  It keeps the tensors alive; make it once."""
-    import torch
     lead = tuple(k_codes.shape[:-1])
     if len(lead) != 3:
         raise ValueError("codes: [batch or pages][n_kv_heads][tokens][64] expected")
-    for name, t, n in (("k_codes", k_codes, 64), ("v_codes", v_codes, 64), ("k_scales", k_scales, 8),
-                       ("v_scales", v_scales, 8)):
-        if t.dtype not in (torch.uint8, torch.float8_e4m3fn if n == 8 else torch.uint8) or tuple(t.shape) != (*lead, n):
-            raise ValueError(f"{name}: u8 {(*lead, n)} expected, got {t.dtype} {tuple(t.shape)}")
-    if page_table is not None:
-        if page_table.dtype != torch.int32 or page_table.dim() != 2:
+    dev = k_codes.get_device()
+    if dev < 0:
+        raise ValueError("libqsa takes CUDA tensors only (no CPU path)")
+    p = [_arg(name, t.view(torch.uint8) if t.dtype is torch.float8_e4m3fn else t, torch.uint8, (*lead, n), dev)
+         for name, t, n in (("k_codes", k_codes, 64), ("k_scales", k_scales, 8), ("v_codes", v_codes, 64),
+                            ("v_scales", v_scales, 8))]
+    table = None
+    if page_table is None:
+        sizes = lead
+    else:
+        if page_table.dim() != 2:
             raise ValueError("page_table: i32 [batch][kv_capacity / page_tokens] expected")
+        table = _arg("page_table", page_table, torch.int32, tuple(page_table.shape), dev)
         if lead[0] != n_pages or lead[2] != page_tokens:
             raise ValueError(f"pools of {n_pages} pages of {page_tokens} tokens expected, got {lead}")
-    cache = qsa_kv4_cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(page_table), page_tokens,
-                          n_pages)
-    cache.lead = lead
-    cache.table_shape = None if page_table is None else tuple(page_table.shape)
+        sizes = (page_table.shape[0], lead[1], page_table.shape[1] * page_tokens)
+    cache = qsa_kv4_cache(*p, table, page_tokens, n_pages)
+    cache.sizes = sizes           # batch, KV heads, capacity: what dims have to say
+    cache.device = dev
     cache.tensors = (k_codes, k_scales, v_codes, v_scales, page_table)
     return cache
 
 
-def _fits(dims, cache):
-    """The cache's sizes are the ones dims give (the C ABI cannot see them)."""
-    if cache.table_shape is None:
-        want, got = (dims.batch, dims.n_kv_heads, dims.kv_capacity), cache.lead
-    else:
-        want = (dims.batch, dims.kv_capacity // cache.page_tokens, dims.n_kv_heads)
-        got = (*cache.table_shape, cache.lead[1])
-    if want != got:
-        raise ValueError(f"cache of sizes {got}, but dims give {want}")
+def _fits(dims, cache, dev):
+    if cache.sizes != (dims.batch, dims.n_kv_heads, dims.kv_capacity):
+        raise ValueError(f"cache of {cache.sizes}, but dims give {(dims.batch, dims.n_kv_heads, dims.kv_capacity)}")
+    if cache.device != dev:
+        raise ValueError(f"cache on cuda:{cache.device}, but the current device is cuda:{dev}")
 
 
 def qsa_kv4_append(dims, cache, k, v, cu_len, len_before, n_tok, workspace=None, stream=None):
     """Round packed K/V rows (bf16 [n_tok][n_kv_heads][128], also slices of a projection) to 4 bits
     into `cache` (kv4_cache): tokens [cu_len[s], cu_len[s+1]) at len_before[s] on."""
-    import torch
-    for name, t in (("k", k), ("v", v)):
-        _like(name, t, torch.bfloat16, (n_tok, dims.n_kv_heads, 128))
-    _like("cu_len", cu_len, torch.int32, (dims.batch + 1,))
-    _like("len_before", len_before, torch.int32, (dims.batch,))
-    _fits(dims, cache)
-    kp, k_ld = _token_rows("k", k, n_tok, dims.n_kv_heads)
-    vp, v_ld = _token_rows("v", v, n_tok, dims.n_kv_heads)
-    _here(cache.tensors[0], k, v, cu_len, len_before, workspace)
-    _check("qsa_kv4_append", load().qsa_kv4_append(
-        ctypes.byref(dims), ctypes.byref(cache), kp, k_ld, vp, v_ld, _ptr(cu_len), _ptr(len_before), n_tok,
-        _ptr(workspace), _stream(stream)))
+    dev, batch, hkv = _device_of(k), dims.batch, dims.n_kv_heads
+    _fits(dims, cache, dev)
+    kp, k_ld = _rows_arg("k", k, n_tok, hkv, dev)
+    vp, v_ld = _rows_arg("v", v, n_tok, hkv, dev)
+    rc = load().qsa_kv4_append(dims, cache, kp, k_ld, vp, v_ld, _arg("cu_len", cu_len, torch.int32, (batch + 1,), dev),
+                               _arg("len_before", len_before, torch.int32, (batch,), dev), n_tok,
+                               _workspace_arg(workspace, dev), _stream(stream))
+    if rc:
+        _check("qsa_kv4_append", rc)
 
 
 def qsa_attn_kv4_plan(dims, n_q, group_q=1):
@@ -399,20 +423,17 @@ def qsa_attn_kv4_plan(dims, n_q, group_q=1):
 def qsa_sparse_attn_kv4(dims, cache, q, q_seq, q_pos, sel_idx, sel_cnt, n_q, out, workspace=None, group_q=1,
                         stream=None):
     """qsa_sparse_attn_ex over a 4-bit cache (kv4_cache); needs no workspace but for its status."""
-    import torch
-    _fits(dims, cache)
-    groups = n_q // max(group_q, 1)
-    for name, t, dtype, shape in (("q", q, torch.bfloat16, (n_q, dims.n_q_heads, 128)),
-                                  ("out", out, torch.bfloat16, (n_q, dims.n_q_heads, 128)),
-                                  ("q_seq", q_seq, torch.int32, (n_q,)), ("q_pos", q_pos, torch.int32, (n_q,)),
-                                  ("sel_idx", sel_idx, torch.int32, (groups, QSA_SEL_CAP)),
-                                  ("sel_cnt", sel_cnt, torch.int32, (groups,))):
-        _like(name, t, dtype, shape)
-    _here(cache.tensors[0], q, q_seq, q_pos, sel_idx, sel_cnt, out, workspace)
-    args = qsa_attn_args(_ptr(q), None, None, _ptr(q_seq), _ptr(q_pos), _ptr(sel_idx), _ptr(sel_cnt), n_q, group_q,
-                         None, 0, 0, _ptr(out))
-    _check("qsa_sparse_attn_kv4", load().qsa_sparse_attn_kv4(
-        ctypes.byref(dims), ctypes.byref(cache), ctypes.byref(args), _ptr(workspace), _stream(stream)))
+    dev, rows = _device_of(q), (n_q, dims.n_q_heads, 128)
+    _fits(dims, cache, dev)
+    groups, i32 = n_q // group_q if group_q > 1 else n_q, torch.int32
+    args = qsa_attn_args(_arg("q", q, torch.bfloat16, rows, dev), None, None, _arg("q_seq", q_seq, i32, (n_q,), dev),
+                         _arg("q_pos", q_pos, i32, (n_q,), dev),
+                         _arg("sel_idx", sel_idx, i32, (groups, QSA_SEL_CAP), dev),
+                         _arg("sel_cnt", sel_cnt, i32, (groups,), dev), n_q, group_q, None, 0, 0,
+                         _arg("out", out, torch.bfloat16, rows, dev))
+    rc = load().qsa_sparse_attn_kv4(dims, cache, args, _workspace_arg(workspace, dev), _stream(stream))
+    if rc:
+        _check("qsa_sparse_attn_kv4", rc)
 
 
 # ---------------------------------------------------------------- pages of a paged cache
@@ -426,8 +447,9 @@ def page_pools(pools, page_tokens, n_pages):
     for i, t in enumerate(pools):
         if t.shape[0] != n_pages:
             raise ValueError(f"pool {i}: {n_pages} pages expected, got {tuple(t.shape)}")
-        p.pool[i] = _ptr(t)
+        p.pool[i] = _arg(f"pool {i}", t, t.dtype, tuple(t.shape), pools[0].get_device())
         p.page_bytes[i] = t.numel() // n_pages * t.element_size()
+    p.device = pools[0].get_device() if pools else None
     p.tensors = tuple(pools)
     return p
 
@@ -436,38 +458,45 @@ def qsa_pages_workspace_bytes(dims, page_tokens, n_pages):
     return int(load().qsa_pages_workspace_bytes(ctypes.byref(dims), page_tokens, n_pages))
 
 
-def _page_state(dims, pools, page_table, page_ref, *more):
-    import torch
-    _like("page_table", page_table, torch.int32, (dims.batch, dims.kv_capacity // pools.page_tokens))
-    _like("page_ref", page_ref, torch.int32, (pools.n_pages,))
-    _here(page_table, page_ref, *pools.tensors[:1], *more)
+def _page_state(dims, pools, page_table, page_ref, dev):
+    if pools.device is not None and pools.device != dev:
+        raise ValueError(f"pools on cuda:{pools.device}, but the current device is cuda:{dev}")
+    return (_arg("page_table", page_table, torch.int32, (dims.batch, dims.kv_capacity // pools.page_tokens), dev),
+            _arg("page_ref", page_ref, torch.int32, (pools.n_pages,), dev))
+
+
+def _list_arg(name, t, n, dev):
+    """Pointer of the first n of a list of sequences."""
+    if n <= 0:
+        return None
+    if t is None or t.dim() != 1 or t.numel() < n:
+        raise ValueError(f"{name}: {n} int32 values expected")
+    return _arg(name, t, torch.int32, t.shape, dev)
 
 
 def qsa_pages_update(dims, pools, page_table, page_ref, len_before, len_after, workspace, free_seq=None, n_free=0,
                      fork_src=None, fork_dst=None, n_fork=0, stream=None):
     """A scheduler's step on a paged cache (page_pools): free sequences, fork others, then make every
     page of positions [len_before, len_after) the sequence's own, copying what was shared."""
-    import torch
-    for name, t, n in (("free_seq", free_seq, n_free), ("fork_src", fork_src, n_fork), ("fork_dst", fork_dst, n_fork)):
-        if n > 0 and (t is None or t.dtype != torch.int32 or t.numel() < n):
-            raise ValueError(f"{name}: {n} int32 values expected")
-    _like("len_before", len_before, torch.int32, (dims.batch,))
-    _like("len_after", len_after, torch.int32, (dims.batch,))
-    _page_state(dims, pools, page_table, page_ref, len_before, len_after, workspace, free_seq, fork_src, fork_dst)
-    _check("qsa_pages_update", load().qsa_pages_update(
-        ctypes.byref(dims), ctypes.byref(pools), _ptr(page_table), _ptr(page_ref), _ptr(free_seq) if n_free else None,
-        n_free, _ptr(fork_src) if n_fork else None, _ptr(fork_dst) if n_fork else None, n_fork, _ptr(len_before),
-        _ptr(len_after), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev, i32, batch = _device_of(page_table), torch.int32, (dims.batch,)
+    table, ref = _page_state(dims, pools, page_table, page_ref, dev)
+    rc = load().qsa_pages_update(
+        dims, pools, table, ref, _list_arg("free_seq", free_seq, n_free, dev), n_free,
+        _list_arg("fork_src", fork_src, n_fork, dev), _list_arg("fork_dst", fork_dst, n_fork, dev), n_fork,
+        _arg("len_before", len_before, i32, batch, dev), _arg("len_after", len_after, i32, batch, dev),
+        _workspace_arg(workspace, dev), workspace.nbytes, _stream(stream))
+    if rc:
+        _check("qsa_pages_update", rc)
 
 
 def qsa_pages_compact(dims, pools, page_table, page_ref, n_live, workspace, stream=None):
     """Move the live pages of every pool to the ids [0, n_live) (n_live: i32 [1], written)."""
-    import torch
-    _like("n_live", n_live, torch.int32, (1,))
-    _page_state(dims, pools, page_table, page_ref, n_live, workspace)
-    _check("qsa_pages_compact", load().qsa_pages_compact(
-        ctypes.byref(dims), ctypes.byref(pools), _ptr(page_table), _ptr(page_ref), _ptr(n_live), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream)))
+    dev = _device_of(page_table)
+    table, ref = _page_state(dims, pools, page_table, page_ref, dev)
+    rc = load().qsa_pages_compact(dims, pools, table, ref, _arg("n_live", n_live, torch.int32, (1,), dev),
+                                  _workspace_arg(workspace, dev), workspace.nbytes, _stream(stream))
+    if rc:
+        _check("qsa_pages_compact", rc)
 
 
 # ---------------------------------------------------------------- context parallelism (see include/qsa.h)

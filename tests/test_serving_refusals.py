@@ -41,28 +41,58 @@ def test_prompt_refusals(qsa):
     assert call(n_tok=0, q=None, out=None) == qsa.QSA_OK
 
 
-def test_prompt_binding_checks_types_shapes_and_strides(qsa):
-    d = _dims(qsa, n_q_heads=2, n_kv_heads=1, batch=1)
+class _On:
+    """A CPU tensor that says it lies on a CUDA device."""
+
+    def __init__(self, t, dev=0):
+        self.t, self.dev = t, dev
+
+    def get_device(self):
+        return self.dev
+
+    def view(self, *a):
+        return _On(self.t.view(*a), self.dev)
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def _on(*s, dtype=torch.int32, dev=0):
+    return _On(torch.zeros(s, dtype=dtype), dev)
+
+
+@pytest.fixture
+def device0(qsa, monkeypatch):
+    monkeypatch.setattr(qsa, "_current_device", lambda: 0)
+
+
+def test_prompt_binding_checks_types_shapes_strides_and_devices(qsa, device0):
+    d = _dims(qsa, n_q_heads=2, n_kv_heads=2, batch=1)
     bf = torch.bfloat16
-    q, k, cu = torch.zeros(5, 2, 128, dtype=bf), torch.zeros(5, 1, 128, dtype=bf), torch.zeros(2, dtype=torch.int32)
-    for bad in (dict(q=q.float()), dict(k=k[:4]), dict(q=q[:, :1])):
-        a = {**dict(q=q, k=k, v=k), **bad}
+    good = dict(q=_on(5, 2, 128, dtype=bf), k=_on(5, 2, 128, dtype=bf), v=_on(5, 2, 128, dtype=bf), cu=_on(2),
+                out=_on(5, 2, 128, dtype=bf))
+
+    def call(**kw):
+        a = {**good, **kw}
+        qsa.qsa_prompt_attn(d, a["q"], a["k"], a["v"], a["cu"], 5, a["out"], a.get("ws"))
+
+    for bad in (dict(q=_on(5, 2, 128)), dict(k=_on(4, 2, 128, dtype=bf)), dict(v=_on(5, 1, 128, dtype=bf)), dict(cu=_on(3)),
+                dict(out=_on(5, 2, 64, dtype=bf))):
         with pytest.raises(ValueError, match="expected"):
-            qsa.qsa_prompt_attn(d, a["q"], a["k"], a["v"], cu, 5, q)
+            call(**bad)
+    apart = _On(torch.zeros(5, 128, 2, dtype=bf).transpose(1, 2))
+    with pytest.raises(ValueError, match="heads of a token"):
+        call(k=apart)
+    with pytest.raises(ValueError, match="contiguous"):
+        call(out=apart)
     with pytest.raises(ValueError, match="CUDA"):
-        qsa.qsa_prompt_attn(d, q, k, k, cu, 5, q)
-
-
-def test_tensors_of_another_device_are_refused(qsa, monkeypatch):
-    class Far:
-        is_cuda = True
-        device = torch.device("cuda", 1)
-
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+        call(q=good["q"].t)
+    for name in good:
+        x = good[name]
+        with pytest.raises(ValueError, match="current device"):
+            call(**{name: _On(x.t, 1)})
     with pytest.raises(ValueError, match="current device"):
-        qsa._here(None, Far())
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    qsa._here(None, Far())
+        call(ws=_on(256, dtype=torch.uint8, dev=1))
 
 
 def _cache(qsa, **kw):
@@ -112,24 +142,43 @@ def test_kv4_attention_refusals(qsa):
     assert call(n_q=0, q=None) == qsa.QSA_OK
 
 
-def test_kv4_binding_checks_the_cache(qsa, monkeypatch):
-    monkeypatch.setattr(qsa, "_ptr", lambda t: None if t is None else 16)
-    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
-    c = qsa.kv4_cache(u8(4, 2, 64, 64), u8(4, 2, 64, 8), u8(4, 2, 64, 64), u8(4, 2, 64, 8))
-    qsa._fits(_dims(qsa, n_q_heads=4, n_kv_heads=2, kv_capacity=64), c)
-    for kw in (dict(batch=5), dict(n_kv_heads=1), dict(kv_capacity=128)):
+def test_kv4_binding_checks_the_cache(qsa, device0):
+    u8 = lambda *s: _on(*s, dtype=torch.uint8)  # noqa: E731
+    small = dict(n_q_heads=4, n_kv_heads=2, kv_capacity=64)
+    c = qsa.kv4_cache(u8(4, 2, 64, 64), u8(4, 2, 64, 8), u8(4, 2, 64, 64), _on(4, 2, 64, 8, dtype=torch.float8_e4m3fn))
+    qsa._fits(_dims(qsa, **small), c, 0)
+    for kw in (dict(batch=5), dict(n_q_heads=1, n_kv_heads=1), dict(kv_capacity=128)):
         with pytest.raises(ValueError, match="dims give"):
-            qsa._fits(_dims(qsa, **{**dict(n_q_heads=4, n_kv_heads=2, kv_capacity=64), **kw}), c)
-    table = torch.zeros((4, 4), dtype=torch.int32)
+            qsa._fits(_dims(qsa, **{**small, **kw}), c, 0)
+    with pytest.raises(ValueError, match="current device"):
+        qsa._fits(_dims(qsa, **small), c, 1)
+    table = _on(4, 4)
     pages = (u8(9, 2, 16, 64), u8(9, 2, 16, 8), u8(9, 2, 16, 64), u8(9, 2, 16, 8))
     p = qsa.kv4_cache(*pages, table, 16, 9)
-    qsa._fits(_dims(qsa, n_q_heads=4, n_kv_heads=2, kv_capacity=64), p)
+    qsa._fits(_dims(qsa, **small), p, 0)
     with pytest.raises(ValueError, match="dims give"):
-        qsa._fits(_dims(qsa, n_q_heads=4, n_kv_heads=2, kv_capacity=80), p)
-    for bad in ((pages[0], pages[1], pages[2], pages[1][:4], table, 16, 9), (pages[0].int(), *pages[1:], table, 16, 9),
-                (*pages, table.long(), 16, 9), (*pages, table, 16, 8), (*pages, table, 32, 9)):
-        with pytest.raises(ValueError):
+        qsa._fits(_dims(qsa, **{**small, "kv_capacity": 80}), p, 0)
+    for bad in ((pages[0], pages[1], pages[2], u8(4, 2, 16, 8), table, 16, 9), (_on(9, 2, 16, 64), *pages[1:], table, 16, 9),
+                (*pages, _on(4, 4, dtype=torch.int64), 16, 9), (*pages, _on(16), 16, 9), (*pages, table, 16, 8),
+                (*pages, table, 32, 9)):
+        with pytest.raises(ValueError, match="expected"):
             qsa.kv4_cache(*bad)
+    with pytest.raises(ValueError, match="current device"):
+        qsa.kv4_cache(*pages, _on(4, 4, dev=1), 16, 9)
+    with pytest.raises(ValueError, match="CUDA"):
+        qsa.kv4_cache(*(x.t for x in pages), table, 16, 9)
+    # the calls: every array's type and size
+    d, bf = _dims(qsa, **small), torch.bfloat16
+    rows = dict(q=_on(6, 4, 128, dtype=bf), q_seq=_on(6), q_pos=_on(6), sel_idx=_on(3, 512), sel_cnt=_on(3), n_q=6,
+                out=_on(6, 4, 128, dtype=bf), group_q=2)
+    for bad in (dict(q=_on(6, 2, 128, dtype=bf)), dict(q_seq=_on(5)), dict(q_pos=_on(6, dtype=torch.int64)),
+                dict(sel_idx=_on(6, 512)), dict(sel_cnt=_on(6)), dict(out=_on(6, 4, 128))):
+        with pytest.raises(ValueError, match="expected"):
+            qsa.qsa_sparse_attn_kv4(d, p, **{**rows, **bad})
+    tok = dict(k=_on(5, 2, 128, dtype=bf), v=_on(5, 2, 128, dtype=bf), cu_len=_on(5), len_before=_on(4), n_tok=5)
+    for bad in (dict(k=_on(5, 4, 128, dtype=bf)), dict(v=_on(6, 2, 128, dtype=bf)), dict(cu_len=_on(4)), dict(len_before=_on(5))):
+        with pytest.raises(ValueError, match="expected"):
+            qsa.qsa_kv4_append(d, p, **{**tok, **bad})
 
 
 def test_kv4_plans_fit_the_hardware(qsa):
@@ -196,22 +245,22 @@ def test_pages_refusals(qsa):
         assert qsa.qsa_pages_workspace_bytes(*bad) == 0
 
 
-def test_pages_binding_checks(qsa, monkeypatch):
-    monkeypatch.setattr(qsa, "_ptr", lambda t: None if t is None else 16)
+def test_pages_binding_checks(qsa, device0):
     d = _dims(qsa)
-    p = qsa.page_pools([torch.zeros(7, 4, 16, 128, dtype=torch.bfloat16), torch.zeros(7, 4, 16, 8, dtype=torch.uint8)], 16, 7)
+    p = qsa.page_pools([_on(7, 4, 16, 128, dtype=torch.bfloat16), _on(7, 4, 16, 8, dtype=torch.uint8)], 16, 7)
     assert list(p.page_bytes[:2]) == [4 * 16 * 256, 4 * 16 * 8] and p.n_pools == 2
     with pytest.raises(ValueError, match="pages expected"):
-        qsa.page_pools([torch.zeros(6, 16)], 16, 7)
+        qsa.page_pools([_on(6, 16)], 16, 7)
     with pytest.raises(ValueError, match="at most"):
-        qsa.page_pools([torch.zeros(7, 16)] * 129, 16, 7)
-    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
-    table, ref, n4 = i32(4, 256), i32(7), i32(4)
-    for bad in (dict(table=i32(4, 255)), dict(ref=i32(8)), dict(before=i32(5)), dict(after=n4.long()), dict(n_free=1),
-                dict(n_fork=5, src=n4, dst=n4)):
+        qsa.page_pools([_on(7, 16)] * 129, 16, 7)
+    table, ref, n4, ws = _on(4, 256), _on(7), _on(4), _on(16, dtype=torch.uint8)
+    for bad in (dict(table=_on(4, 255)), dict(ref=_on(8)), dict(before=_on(5)), dict(after=_on(4, dtype=torch.int64)),
+                dict(n_free=1), dict(n_fork=5, src=n4, dst=n4), dict(n_fork=4, src=n4, dst=_on(4, dtype=torch.int64))):
         a = {**dict(table=table, ref=ref, before=n4, after=n4, n_free=0, src=None, dst=None, n_fork=0), **bad}
         with pytest.raises(ValueError, match="expected"):
-            qsa.qsa_pages_update(d, p, a["table"], a["ref"], a["before"], a["after"], torch.zeros(16), n_free=a["n_free"],
+            qsa.qsa_pages_update(d, p, a["table"], a["ref"], a["before"], a["after"], ws, n_free=a["n_free"],
                                  fork_src=a["src"], fork_dst=a["dst"], n_fork=a["n_fork"])
     with pytest.raises(ValueError, match="n_live"):
-        qsa.qsa_pages_compact(d, p, table, ref, i32(2), torch.zeros(16))
+        qsa.qsa_pages_compact(d, p, table, ref, _on(2), ws)
+    with pytest.raises(ValueError, match="current device"):
+        qsa.qsa_pages_compact(d, p, table, _on(7, dev=1), _on(1), ws)
