@@ -6,8 +6,8 @@
 // layer is exactly this (keieiax.jp glossary "Qwen Sparse Attention", section on cost:
 // dense GQA is what the sparse layer is compared with), and every prompt starts there.
 //
-// Work unit: one CTA per (query tile pair, KV head).  A query tile is 128 MMA rows, the
-// floor(128 / G) consecutive tokens whose G query heads read the same K and V; a CTA has
+// Work unit: one item per (query tile pair, KV head).  A query tile is 128 MMA rows, the
+// floor(128 / G) consecutive tokens whose G query heads read the same K and V; an item has
 // two of them (A, then B), so each K and V tile in shared memory feeds 256 rows, a
 // prompt of a few tokens fills one tile with all its heads, and the causal triangle
 // wastes at most one key tile per 2 x floor(128 / G) tokens.
@@ -15,13 +15,18 @@
 // One pass over the keys with a running maximum m and sum l (exp2 domain):
 //     S = Q K^T;  P = exp2(scale log2(e) S - m);  l = l f + sum P;  O = O f + P V.
 // m only moves when a row's maximum grew by more than 8 (a factor of 256 in P, which
-// fp32 sums and bf16 P carry without loss): the factor f is 1 in almost every step, and
-// O, which lies in TMEM, is read and written back only in the others.
+// fp32 sums and bf16 P carry without loss), so the factor f is 1 in almost every step:
+// the exponentials start from the old m while the new maximum is still being taken, and
+// O, which lies in TMEM, is read and written back only where m moved.
 //
-// CTA = 12 warps, one CTA per SM (512 TMEM columns: S of A and B, O of A and B, 128
-// each; P overwrites its own S as packed bf16):
-//   warp 0       TMA producer: the two query tiles, then K and V tiles of 128 tokens
-//                (32 KiB, 128-byte swizzle) through a ring of 5;
+// The grid has one CTA per item, but a CTA that finishes an item takes the next one off
+// the queue of CTAs that have not started (cluster launch control): barriers and TMEM are
+// set up once per SM, the next item's tiles load during the last steps of the current one,
+// and items of very different length balance.  CTA = 12 warps, one CTA per SM (512 TMEM
+// columns: S of A and B, O of A and B, 128 each; P overwrites its own S as packed bf16):
+//   warp 0       takes items, finds their sequence and loads them by TMA: the two query
+//                tiles, then K and V tiles of 128 tokens (32 KiB, 128-byte swizzle) through
+//                a ring of 5;
 //   warp 1       MMA issuer (and TMEM allocator): per key tile P_A V, S_A of the next
 //                tile, P_B V, S_B of the next tile, so one tile's MMAs run while the
 //                other tile's softmax does.  tcgen05 MMAs of one thread execute in
@@ -32,12 +37,13 @@
 //                into rows that must not see the token), and the first token holding
 //                one is kept per dim; the epilogue gives it back to the rows behind it;
 //   warps 4-11   softmax, four warps per query tile, one row per thread: S from TMEM,
-//                maximum, exponentials, P back to TMEM; at the end O / l to global
-//                memory through the tile's query buffer.
+//                exponentials, P back to TMEM in two parts (the MMA starts on the first);
+//                at the end O / l to global memory, 32 bytes per store.
 // Every wait is bounded (QSA_DEV_TIMEOUT, drain, free TMEM, return).
 
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "sm100_host.cuh"
 #include "sm100_ptx.cuh"
@@ -51,25 +57,40 @@ namespace {
 constexpr int kRows = 128;                // MMA rows of a query tile
 constexpr int kKeys = 128;                // tokens of a K or V tile
 constexpr int kRing = 5;                  // K and V tiles in flight
+constexpr int kItems = 4;                 // items known at once: the producer's ring reaches at most three ahead
+constexpr int kGuards = 4;                // masked V tiles known at once: at most three of the ring's tiles are V
 constexpr int kThreads = 384;
+constexpr int kReaders = 1 + 2 + 8;       // warps that read an item: MMA, guard, softmax
 constexpr int kHalf = kRows * 64;         // values of one 64-dim half of a tile
 constexpr uint32_t kTileBytes = kKeys * kHeadDim * 2;
 constexpr uint32_t kTmemColsPrompt = 512;
 constexpr uint32_t kColO = 256;           // TMEM column of O of tile A (S of A, S of B before it)
 constexpr float kGrow = 8.0f;             // growth of a row maximum (log2) that rescales O
+constexpr int kPolyEvery = 4;             // one pair of exponentials in this many goes to the FMA pipes
+constexpr int kEarly = 3;                 // quarters of P that the MMA may read before the last one is there
+static_assert(kEarly == 3, "the maxima of quarter 3 are taken with those of quarter 1");
 
 enum { kPosInf = 0, kNegInf = 1, kNan = 2 };
 
+struct Item {
+    int len;                              // of the sequence; 0: no more items
+    int tok0;                             // its first packed token
+    int t0;                               // first token of tile A, in the sequence
+    int head;                             // KV head
+};
+
 struct __align__(1024) PromptSmem {
-    __nv_bfloat16 q[2][2][kHalf];         // [tile][dim half]; the tile's output at the end
+    __nv_bfloat16 q[2][2][kHalf];         // [tile][dim half]
     __nv_bfloat16 kv[kRing][2][kHalf];    // K and V tiles in turn
-    int bad[3][kHeadDim];                 // first token of the masked tiles whose V is +inf, -inf, NaN
-    uint64_t q_full[2], kv_full[kRing], kv_empty[kRing];
-    uint64_t s_full[2], p_full[2], o_full[2], mma_done;
-    uint64_t v_full[2], v_clean[2];       // masked V tiles: landed, guarded
+    uint4 next;                           // answer of the launch control
+    Item item[kItems];
+    int bad[3][kHeadDim];                 // first token of the item's masked tiles whose V is +inf, -inf, NaN
+    uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing];
+    uint64_t s_full[2], p_full[2][2], o_full[2];   // P in two parts
+    uint64_t v_full[kGuards], v_clean[kGuards];    // masked V tiles: landed, guarded
+    uint64_t item_full[kItems], item_empty[kItems], next_full, item_done, mma_done;
     uint32_t tmem_base;
     int error, any_bad;
-    int tok0, t0, len;                    // first packed token, first token of tile A, length of the sequence
 };
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -93,348 +114,554 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
     return d;
 }
 
+// 2^x of two values on the FMA pipes: x = n + f with n the nearest integer (by adding and
+// taking away 1.5 * 2^23), 2^f a cubic with p(0) = 1 whose largest relative error on
+// [-1/2, 1/2] is as small as a cubic's can be (least squares reweighted to it: 2^-13.2, a
+// sixteenth of P's bf16 rounding), 2^n by adding n to the exponent.  x below -127 counts as
+// -127, which gives 0; x must not be NaN and stay below 128.
+__device__ __forceinline__ void exp2_poly2(unsigned long long x2, float& p0, float& p1)
+{
+    constexpr float kMagic = 12582912.0f;
+    const float x0 = fmaxf(__uint_as_float((unsigned)x2), -127.0f);
+    const float x1 = fmaxf(__uint_as_float((unsigned)(x2 >> 32)), -127.0f);
+    const unsigned long long x = pack2(x0, x1);
+    const unsigned long long t = add2(x, pack2(kMagic, kMagic));
+    const unsigned long long n = add2(t, pack2(-kMagic, -kMagic));
+    const unsigned long long f = fma2(n, pack2(-1.0f, -1.0f), x);
+    unsigned long long p = fma2(f, pack2(0.05500893f, 0.05500893f), pack2(0.24221097f, 0.24221097f));
+    p = fma2(p, f, pack2(0.6932829f, 0.6932829f));
+    p = fma2(p, f, pack2(1.0f, 1.0f));
+    p0 = __uint_as_float((unsigned)p + ((unsigned)t << 23));
+    p1 = __uint_as_float((unsigned)(p >> 32) + ((unsigned)(t >> 32) << 23));
+}
+
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Take the next CTA of the grid that has not started; 16 bytes of answer arrive on `bar`.
+__device__ __forceinline__ void take_next_cta(uint4* answer, uint64_t* bar)
+{
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];\n" ::"r"(
+            smem_u32(answer)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+
+// blockIdx.x of the CTA taken, or -1 if there was none.
+__device__ __forceinline__ int taken_cta(const uint4* answer)
+{
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "mov.b32 %1, 0;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}\n"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return ok ? (int)x : -1;
+}
+
+__device__ __forceinline__ void store_32b(void* p, const uint32_t (&w)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1)
 k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
               const __grid_constant__ CUtensorMap tmap_v, const int32_t* __restrict__ cu_len, int batch, int n_tok,
-              int n_q_heads, int n_kv_heads, int64_t n_tiles, float scale_log2, __nv_bfloat16* __restrict__ out,
+              int n_q_heads, int n_kv_heads, int n_tiles, float scale_log2, __nv_bfloat16* __restrict__ out,
               unsigned* status)
 {
     extern __shared__ uint8_t smem_raw[];
     PromptSmem& S = *reinterpret_cast<PromptSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int G = n_q_heads / n_kv_heads;
     const int ta = kRows / G;                              // tokens of a query tile
     const int tq = 2 * ta;
-    const int head = blockIdx.x % n_kv_heads;
-    const int64_t x = n_tiles - 1 - blockIdx.x / n_kv_heads;   // the longest rows of each sequence first
 
-    if (warp == 0) {
-        // sequence s's tiles start at index cu[s] / tq + s, which leaves every sequence at least
-        // ceil(len / tq) indices and needs no prefix sum
-        const int s = find_sequence(batch, lane, [&](int i) { return (int64_t)(__ldg(cu_len + i) / tq) + i <= x; });
-        if (lane == 0) {
-            int t0 = 0, len = 0, tok0 = 0;
-            if (s >= 0) {
-                const int a = __ldg(cu_len + s), b = __ldg(cu_len + s + 1);
-                if (a >= 0 && a <= b && b <= n_tok) {
-                    const int64_t first = (x - (a / tq + s)) * tq;
-                    tok0 = a;
-                    len = first >= 0 && first < b - a ? b - a : 0;
-                    t0 = len > 0 ? (int)first : 0;
-                }
-            }
-            S.tok0 = tok0;
-            S.t0 = t0;
-            S.len = len;
-            S.error = 0;
-            S.any_bad = 0;
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&S.q_full[i], 1);
-                mbar_init(&S.s_full[i], 1);
-                mbar_init(&S.p_full[i], 4);                // one arrival per softmax warp
-                mbar_init(&S.o_full[i], 1);
-                mbar_init(&S.v_full[i], 1);
-                mbar_init(&S.v_clean[i], 2);               // one arrival per guard warp
-            }
-            for (int i = 0; i < kRing; ++i) {
-                mbar_init(&S.kv_full[i], 1);
-                mbar_init(&S.kv_empty[i], 1);
-            }
-            mbar_init(&S.mma_done, 1);
-            fence_mbar_init();
-        }
+    if (warp == 0 && lane == 0) {
+        prefetch_tensormap(&tmap_q);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
     }
-    // malformed lengths are skipped above; the first CTA reports them
-    if (blockIdx.x == 0)
-        for (int s = tid; s < batch; s += kThreads) {
-            const int a = __ldg(cu_len + s), b = __ldg(cu_len + s + 1);
-            if (a < 0 || a > b || b > n_tok) set_status(status, QSA_DEV_BAD_LEN);
-        }
-    for (int k = tid; k < 3 * kHeadDim; k += kThreads) (&S.bad[0][0])[k] = INT_MAX;
-    __syncthreads();
-    const int len = S.len, t0 = S.t0, tok0 = S.tok0;
-    if (len == 0) return;                                  // an index no tile has
     if (warp == 1) {
         tmem_alloc(&S.tmem_base, kTmemColsPrompt);
         tmem_relinquish();
     }
+    if (warp == 2 && lane == 0) {
+        S.error = 0;
+        S.any_bad = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.q_full[i], 1);
+            mbar_init(&S.q_empty[i], 1);
+            mbar_init(&S.s_full[i], 1);
+            mbar_init(&S.p_full[i][0], 4);                 // one arrival per softmax warp
+            mbar_init(&S.p_full[i][1], 4);
+            mbar_init(&S.o_full[i], 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&S.kv_full[i], 1);
+            mbar_init(&S.kv_empty[i], 1);
+        }
+        for (int i = 0; i < kGuards; ++i) {
+            mbar_init(&S.v_full[i], 1);
+            mbar_init(&S.v_clean[i], 2);                   // one arrival per guard warp
+        }
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&S.item_full[i], 1);
+            mbar_init(&S.item_empty[i], kReaders);
+        }
+        mbar_init(&S.next_full, 1);
+        mbar_init(&S.item_done, 8);                        // one arrival per softmax warp
+        mbar_init(&S.mma_done, 1);
+        fence_mbar_init();
+    }
+    for (int k = tid; k < 3 * kHeadDim; k += kThreads) (&S.bad[0][0])[k] = INT_MAX;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = S.tmem_base;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, S.tmem_base, 0);   // the same in every lane, for the uniform datapath
     volatile int* err = &S.error;
 
-    // key tiles of each query tile (B may have one more than A, or none)
-    const int n_a = (min(t0 + ta, len) - 1) / kKeys + 1;
-    const int n_b = t0 + ta < len ? (min(t0 + 2 * ta, len) - 1) / kKeys + 1 : 0;
-    const int n_kv = max(n_a, n_b);
-    // first key tile that some row masks; there are one or two of them: a CTA's tokens
-    // number at most 128, or 256 that start at a multiple of 256 (G = 1)
-    const int j_mask = t0 / kKeys;
-    // barrier that ring tile k (K_0, V_0, K_1, ...) lands on.  Masked V tiles have one each
-    // that the guard can wait on without following the ring's phases; no later tile uses
-    // their slots (at most three tiles come after the first of them)
-    auto landed = [&](int k) {
-        const int m = (k >> 1) - j_mask;
-        return (k & 1) && m >= 0 ? &S.v_full[m] : &S.kv_full[k % kRing];
+    // What a role needs of an item.  Key tiles of A and of B (one more than A's, or as many, or
+    // none); first key tile that some row masks: it and the last one are one or two tiles,
+    // since an item's tokens number at most 128, or 256 from a multiple of 256 (G = 1).
+    struct Tiles {
+        int n_a, n_b, n_kv, j_mask;
     };
-    auto parity = [&](int k) { return (uint32_t)((k & 1) && (k >> 1) >= j_mask ? 0 : (k / kRing) & 1); };
+    auto tiles_of = [&](const Item& it) {
+        Tiles t;
+        t.n_a = (min(it.t0 + ta, it.len) - 1) / kKeys + 1;
+        t.n_b = it.t0 + ta < it.len ? (min(it.t0 + 2 * ta, it.len) - 1) / kKeys + 1 : 0;
+        t.n_kv = max(t.n_a, t.n_b);
+        t.j_mask = it.t0 / kKeys;
+        return t;
+    };
+    // item number n of this CTA, read by a whole warp; len 0: there are no more
+    auto read_item = [&](int n, Item& it) {
+        it.len = 0;
+        if (!wait_phase(&S.item_full[n % kItems], (n / kItems) & 1, err, status)) return false;
+        it = S.item[n % kItems];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.item_empty[n % kItems]);
+        return it.len > 0;
+    };
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
         if (warp == 0) {
-            if (lane == 0) {
-                prefetch_tensormap(&tmap_q);
-                prefetch_tensormap(&tmap_k);
-                prefetch_tensormap(&tmap_v);
-                int issued = 0;
-                auto load_q = [&](int i) {
-                    mbar_arrive_expect_tx(&S.q_full[i], (uint32_t)(ta * G) * kHeadDim * 2);
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_3d(S.q[i][h], &tmap_q, &S.q_full[i], 64 * h, head * G, tok0 + t0 + i * ta);
-                };
-                for (int k = 0; k < 2 * n_kv; ++k) {
-                    const int slot = k % kRing;
-                    if (k == 0) load_q(0);
-                    if (k >= kRing && !wait_phase(&S.kv_empty[slot], ((k / kRing) - 1) & 1, err, status)) break;
-                    mbar_arrive_expect_tx(landed(k), kTileBytes);
-                    for (int h = 0; h < 2; ++h)
-                        tma_load_3d(S.kv[slot][h], (k & 1) ? &tmap_v : &tmap_k, landed(k), 64 * h, head,
-                                    tok0 + (k >> 1) * kKeys);
-                    issued = k + 1;
-                    if (k == 0 && n_b > 0) load_q(1);
+            // ---------------- items and loads ----------------
+            int cta = blockIdx.x, k_ring = 0, n_mask = 0, asked = 0, n_item = 0;
+            bool ok = true, more = true;
+            while (ok && more) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&S.next_full, 16);
+                    take_next_cta(&S.next, &S.next_full);
+                    // malformed lengths are skipped below and reported here: the grid has more
+                    // indices than there are sequences, and each is somebody's once
+                    if (cta < batch) {
+                        const int a = __ldg(cu_len + cta), b = __ldg(cu_len + cta + 1);
+                        if (a < 0 || a > b || b > n_tok) set_status(status, QSA_DEV_BAD_LEN);
+                    }
                 }
-                if (*err) {
-                    // drain: every issued tile must land before the CTA exits
-                    for (int i = 0; i < (n_b > 0 ? 2 : 1); ++i) {
-                        const uint64_t t = now_ns();
-                        while (!mbar_try_wait(&S.q_full[i], 0) && now_ns() - t < kWaitNs) {
+                ++asked;
+                // the longest rows of each sequence first.  Sequence s's tiles start at index
+                // cu[s] / tq + s, which leaves every sequence at least ceil(len / tq) indices
+                // and needs no prefix sum
+                const int x = n_tiles - 1 - cta / n_kv_heads;
+                const int s = find_sequence(batch, lane, [&](int i) { return __ldg(cu_len + i) / tq + i <= x; });
+                Item it{0, 0, 0, cta % n_kv_heads};
+                if (s >= 0) {
+                    const int a = __ldg(cu_len + s), b = __ldg(cu_len + s + 1);
+                    const int64_t first = (int64_t)(x - (a / tq + s)) * tq;
+                    if (a >= 0 && a <= b && b <= n_tok && first >= 0 && first < b - a) it = Item{b - a, a, (int)first, it.head};
+                }
+                if (it.len > 0) {
+                    const int slot = n_item % kItems;
+                    if (n_item >= kItems && !wait_phase(&S.item_empty[slot], ((n_item / kItems) - 1) & 1, err, status)) break;
+                    if (lane == 0) {
+                        S.item[slot] = it;
+                        mbar_arrive(&S.item_full[slot]);
+                    }
+                    const Tiles t = tiles_of(it);
+                    if (lane == 0) {
+                        auto load_q = [&](int i) {
+                            if (n_item > 0 && !wait_phase(&S.q_empty[i], (n_item - 1) & 1, err, status)) return false;
+                            mbar_arrive_expect_tx(&S.q_full[i], (uint32_t)(ta * G) * kHeadDim * 2);
+                            for (int h = 0; h < 2; ++h)
+                                tma_load_3d(S.q[i][h], &tmap_q, &S.q_full[i], 64 * h, it.head * G, it.tok0 + it.t0 + i * ta);
+                            return true;
+                        };
+                        ok = load_q(0);
+                        for (int k = 0; k < 2 * t.n_kv && ok; ++k) {
+                            const int ring = k_ring % kRing;
+                            if (k_ring >= kRing && !(ok = wait_phase(&S.kv_empty[ring], ((k_ring / kRing) - 1) & 1, err, status)))
+                                break;
+                            // a masked V tile lands on a barrier of its own, which the guard can
+                            // wait on without following the ring
+                            const bool masked = (k & 1) && (k >> 1) >= t.j_mask;
+                            uint64_t* bar = masked ? &S.v_full[n_mask % kGuards] : &S.kv_full[ring];
+                            n_mask += masked;
+                            mbar_arrive_expect_tx(bar, kTileBytes);
+                            tma_load_4d(S.kv[ring], (k & 1) ? &tmap_v : &tmap_k, bar, 0, it.tok0 + (k >> 1) * kKeys, 0, it.head);
+                            ++k_ring;
+                            if (k == 0) ok = load_q(1);    // also for an absent B: its barriers keep step with A's
                         }
                     }
-                    for (int k = max(0, issued - kRing); k < issued; ++k) {
-                        const uint64_t t = now_ns();
-                        while (!mbar_try_wait(landed(k), parity(k)) && now_ns() - t < kWaitNs) {
-                        }
+                    ++n_item;
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                }
+                if (!ok || !(ok = wait_phase(&S.next_full, (asked - 1) & 1, err, status))) break;
+                cta = taken_cta(&S.next);
+                fence_proxy_async();                       // read before the next answer overwrites it
+                __syncwarp();
+                more = cta >= 0;
+            }
+            if (ok) {
+                const int slot = n_item % kItems;
+                if (n_item < kItems || wait_phase(&S.item_empty[slot], ((n_item / kItems) - 1) & 1, err, status))
+                    if (lane == 0) {
+                        S.item[slot].len = 0;
+                        mbar_arrive(&S.item_full[slot]);
                     }
+            } else if (lane == 0) {
+                // drain: what is on its way into shared memory must land before the CTA exits
+                // (1 ms, some thousand times a tile's latency)
+                const uint64_t t = now_ns();
+                while (now_ns() - t < 1000000) {
                 }
             }
         } else if (warp == 1) {
-            if (lane == 0) {
-                constexpr uint32_t id_s = idesc_bf16_f32(kRows, kKeys);
-                constexpr uint32_t id_o = idesc_bf16_f32(kRows, kHeadDim) | kIdescBMnMajor;
-                auto issue_s = [&](int i, int k) {         // S_i = Q_i K^T, 8 K steps over two 64-dim halves
+            // ---------------- MMA ----------------
+            constexpr uint32_t id_s = idesc_bf16_f32(kRows, kKeys);
+            constexpr uint32_t id_o = idesc_bf16_f32(kRows, kHeadDim) | kIdescBMnMajor;
+            const uint32_t me = elect_one();
+            const uint64_t q_desc = smem_desc_sw128(smem_u32(S.q)), k_desc = smem_desc_sw128(smem_u32(S.kv));
+            const uint64_t v_desc = smem_desc_sw128_mn(smem_u32(S.kv), kHalf * 2);
+            constexpr uint32_t kTileDesc = kTileBytes >> 4, kHalfDesc = (kHalf * 2) >> 4;   // descriptor units
+            auto issue_s = [&](int i, int slot) {          // S_i = Q_i K^T, 8 K steps over two 64-dim halves
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint64_t a = smem_desc_sw128(smem_u32(S.q[i][h]));
-                        const uint64_t b = smem_desc_sw128(smem_u32(S.kv[k % kRing][h]));
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t at = (u >> 2) * kHalfDesc + 2 * (u & 3);
+                    mma_bf16_ss_elected(tmem + i * kKeys, q_desc + (i * kTileDesc + at), k_desc + (slot * kTileDesc + at),
+                                        id_s, u > 0, me);
+                }
+                mma_commit_elected(&S.s_full[i], me);
+            };
+            auto issue_o = [&](int i, int slot, bool first, int from, int to) {   // O_i += P_i V, K steps of 16 tokens
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) mma_bf16_ss(tmem + i * kKeys, a + 2 * u, b + 2 * u, id_s, h + u > 0);
+                for (int u = from; u < to; ++u)
+                    mma_bf16_ts_elected(tmem + kColO + i * kHeadDim, tmem + i * kKeys + 8 * u,
+                                        v_desc + (slot * kTileDesc + 128 * u), id_o, !first || u > 0, me);
+            };
+            uint32_t ring_phase = 0;                       // per slot: parity of kv_full's next use
+            auto ring_full = [&](int slot) {
+                const uint32_t ph = (ring_phase >> slot) & 1u;
+                ring_phase ^= 1u << slot;
+                return wait_phase(&S.kv_full[slot], ph, err, status);
+            };
+            auto after = [](int slot, int n) { return slot + n >= kRing ? slot + n - kRing : slot + n; };
+            int k_slot = 0, n_mask = 0, p_phase[2] = {0, 0};
+            Item it;
+            bool ok = true;
+            for (int n = 0; ok && read_item(n, it); ++n) {
+                const Tiles t = tiles_of(it);
+                ok = ring_full(k_slot);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!ok || !(ok = wait_phase(&S.q_full[i], n & 1, err, status))) continue;
+                    tc_fence_after();
+                    const int n_i = i ? t.n_b : t.n_a;
+                    if (n_i > 0) issue_s(i, k_slot);
+                    if (n_i <= 1) mma_commit_elected(&S.q_empty[i], me);
+                }
+                mma_commit_elected(&S.kv_empty[k_slot], me);
+                for (int j = 0; j < t.n_kv && ok; ++j) {
+                    const int v_slot = after(k_slot, 1), k_next = after(k_slot, 2);
+                    const bool more = j + 1 < t.n_kv;
+                    if (j < t.j_mask) {
+                        ok = ring_full(v_slot);
+                    } else {
+                        const int g = n_mask++;
+                        ok = wait_phase(&S.v_full[g % kGuards], (g / kGuards) & 1, err, status) &&
+                             wait_phase(&S.v_clean[g % kGuards], (g / kGuards) & 1, err, status);
                     }
-                    mma_commit(&S.s_full[i]);
-                };
-                auto issue_o = [&](int i, int j) {         // O_i += P_i V, 8 K steps of 16 tokens
-                    const uint64_t b = smem_desc_sw128_mn(smem_u32(S.kv[(2 * j + 1) % kRing][0]), kHalf * 2);
+                    bool k_here = false;
 #pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        mma_bf16_ts(tmem + kColO + i * kHeadDim, tmem + i * kKeys + 8 * u, b + 128 * u, id_o, j + u > 0);
-                };
-                auto ring_full = [&](int k) { return wait_phase(landed(k), parity(k), err, status); };
-                bool ok = ring_full(0);
-                for (int i = 0; i < (n_b > 0 ? 2 : 1) && ok; ++i)
-                    if ((ok = wait_phase(&S.q_full[i], 0, err, status))) {
+                    for (int i = 0; i < 2; ++i) {
+                        const int n_i = i ? t.n_b : t.n_a;
+                        if (!ok || j >= n_i) continue;
+                        const uint32_t ph = (uint32_t)p_phase[i];
+                        p_phase[i] ^= 1;
+                        if (!(ok = wait_phase(&S.p_full[i][0], ph, err, status))) continue;
                         tc_fence_after();
-                        issue_s(i, 0);
-                    }
-                mma_commit(&S.kv_empty[0]);
-                for (int j = 0; j < n_kv && ok; ++j) {
-                    ok = ring_full(2 * j + 1) && (j < j_mask || wait_phase(&S.v_clean[j - j_mask], 0, err, status));
-                    for (int i = 0; i < 2 && ok; ++i) {
-                        const int n_i = i ? n_b : n_a;
-                        if (j >= n_i) continue;
-                        if (!(ok = wait_phase(&S.p_full[i], j & 1, err, status))) break;
+                        issue_o(i, v_slot, j == 0, 0, 2 * kEarly);
+                        if (more && !k_here) {
+                            if (!(ok = ring_full(k_next))) continue;
+                            k_here = true;
+                        }
+                        if (!(ok = wait_phase(&S.p_full[i][1], ph, err, status))) continue;
                         tc_fence_after();
-                        issue_o(i, j);
+                        issue_o(i, v_slot, j == 0, 2 * kEarly, 8);
                         if (j + 1 == n_i) {
-                            mma_commit(&S.o_full[i]);
-                        } else if ((ok = ring_full(2 * j + 2))) {
-                            tc_fence_after();
-                            issue_s(i, 2 * j + 2);
+                            mma_commit_elected(&S.o_full[i], me);
+                        } else {
+                            issue_s(i, k_next);
+                            if (j + 2 == n_i) mma_commit_elected(&S.q_empty[i], me);
                         }
                     }
-                    mma_commit(&S.kv_empty[(2 * j + 1) % kRing]);
-                    if (j + 1 < n_kv) mma_commit(&S.kv_empty[(2 * j + 2) % kRing]);
-                }
-                // every MMA issued must finish before TMEM is released
-                mma_commit(&S.mma_done);
-                const uint64_t t = now_ns();
-                while (!mbar_try_wait(&S.mma_done, 0) && now_ns() - t < kWaitNs) {
+                    mma_commit_elected(&S.kv_empty[v_slot], me);
+                    if (more) mma_commit_elected(&S.kv_empty[k_next], me);
+                    k_slot = k_next;
                 }
             }
+            // every MMA issued must finish before TMEM is released
+            mma_commit_elected(&S.mma_done, me);
+            const uint64_t t = now_ns();
+            while (!mbar_try_wait(&S.mma_done, 0) && now_ns() - t < kWaitNs) {
+            }
         } else {
-            // V guard: 64 threads over the 32 KiB of each masked V tile
+            // ---------------- V guard: 64 threads over the 32 KiB of each masked V tile ----------------
             const int gt = (warp - 2) * 32 + lane;
-            for (int j = j_mask; j < n_kv; ++j) {
-                const int k = 2 * j + 1;
-                if (!wait_phase(&S.v_full[j - j_mask], 0, err, status)) break;
-                uint4* tile = reinterpret_cast<uint4*>(S.kv[k % kRing][0]);
-                bool wrote = false;
-#pragma unroll 4
-                for (int c = gt; c < (int)(kTileBytes / 16); c += 64) {
-                    uint4 v = tile[c];
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t hit = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) hit |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-                    if (hit == 0) continue;
-                    // chunk c: half c >> 10, token row (c >> 3) & 127, swizzled 16-byte chunk c & 7
-                    const int row = (c >> 3) & 127, tok = j * kKeys + row;
-                    const int dim0 = (c >> 10) * 64 + (((c & 7) ^ (row & 7)) << 3);
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t b = (w[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
-                        if ((b & 0x7F80u) != 0x7F80u) continue;
-                        const int kind = (b & 0x7Fu) ? kNan : (b & 0x8000u) ? kNegInf : kPosInf;
-                        atomicMin(&S.bad[kind][dim0 + e], tok);
-                        w[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
-                    }
-                    tile[c] = make_uint4(w[0], w[1], w[2], w[3]);
-                    wrote = true;
+            int k_ring = 0, n_mask = 0;
+            Item it;
+            for (int n = 0; read_item(n, it); ++n) {
+                const Tiles t = tiles_of(it);
+                // the last item's epilogues are done with `bad`
+                if (n > 0 && !wait_phase(&S.item_done, (n - 1) & 1, err, status)) break;
+                if (*(volatile int*)&S.any_bad) {
+                    asm volatile("bar.sync 1, 64;\n" ::: "memory");
+                    for (int k = gt; k < 3 * kHeadDim; k += 64) (&S.bad[0][0])[k] = INT_MAX;
+                    S.any_bad = 0;
+                    asm volatile("bar.sync 1, 64;\n" ::: "memory");
                 }
-                if (wrote) S.any_bad = 1;
-                fence_proxy_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.v_clean[j - j_mask]);
+                bool ok = true;
+                for (int j = t.j_mask; j < t.n_kv && ok; ++j) {
+                    const int g = n_mask++;
+                    if (!(ok = wait_phase(&S.v_full[g % kGuards], (g / kGuards) & 1, err, status))) break;
+                    uint4* tile = reinterpret_cast<uint4*>(S.kv[(k_ring + 2 * j + 1) % kRing][0]);
+                    bool wrote = false;
+#pragma unroll 4
+                    for (int c = gt; c < (int)(kTileBytes / 16); c += 64) {
+                        uint4 v = tile[c];
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t hit = 0;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) hit |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                        if (hit == 0) continue;
+                        // chunk c: half c >> 10, token row (c >> 3) & 127, swizzled 16-byte chunk c & 7
+                        const int row = (c >> 3) & 127, tok = j * kKeys + row;
+                        const int dim0 = (c >> 10) * 64 + (((c & 7) ^ (row & 7)) << 3);
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t b = (w[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
+                            if ((b & 0x7F80u) != 0x7F80u) continue;
+                            const int kind = (b & 0x7Fu) ? kNan : (b & 0x8000u) ? kNegInf : kPosInf;
+                            atomicMin(&S.bad[kind][dim0 + e], tok);
+                            w[e >> 1] &= (e & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+                        }
+                        tile[c] = make_uint4(w[0], w[1], w[2], w[3]);
+                        wrote = true;
+                    }
+                    if (wrote) S.any_bad = 1;
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.v_clean[g % kGuards]);
+                }
+                if (!ok) break;
+                k_ring += 2 * t.n_kv;
             }
         }
     } else {
+        // ---------------- softmax ----------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n");
         const int i = (warp - 4) >> 2;
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
-        const int first = t0 + i * ta;
-        const int tok = first + row / G;                   // rows past ta * G hold nothing and are not stored
-        const int n_own = i ? n_b : n_a;
-        const int j_own = first / kKeys;                   // first key tile this query tile masks
+        const int row_tok = row / G, row_head = row % G;   // rows past ta * G hold nothing and are not stored
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t col_s = lanes + i * kKeys, col_o = lanes + kColO + i * kHeadDim;
         const unsigned long long sc2 = pack2(scale_log2, scale_log2);
-        float m = -INFINITY;
-        unsigned long long l2 = 0ull;                      // two partial sums
+        const bool wide = ((uintptr_t)out & 31u) == 0;     // 32-byte stores
+        int n_step = 0, n_mask = 0, n_o = 0;
+        Item it;
         bool ok = true;
-        for (int j = 0; j < n_own; ++j) {
-            if (!(ok = wait_phase(&S.s_full[i], j & 1, err, status))) break;
-            tc_fence_after();
-            uint32_t v[4][32];
+        for (int n = 0; ok && read_item(n, it); ++n) {
+            const Tiles t = tiles_of(it);
+            const int n_own = i ? t.n_b : t.n_a;
+            const int first = it.t0 + i * ta;
+            const int tok = first + row_tok;
+            const int j_own = first / kKeys;               // first key tile this query tile masks
+            n_mask += t.n_kv - t.j_mask;
+            float m = -INFINITY;
+            unsigned long long l2 = 0ull;                  // two partial sums
+            for (int j = 0; j < n_own; ++j, ++n_step) {
+                if (!(ok = wait_phase(&S.s_full[i], n_step & 1, err, status))) break;
+                tc_fence_after();
+                uint32_t v[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32w(col_s + 32 * c, v[c]);
-            tmem_ld_wait();
-            if (j >= j_own) {
-                const int lim = tok - j * kKeys;           // keys up to lim are seen
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * c + e > lim) v[c][e] = 0xFF800000u;
-            }
-            float mx[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
-#pragma unroll
-                for (int e = 2; e < 32; e += 2) mx[c] = max3(mx[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
-            }
-            const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale_log2;
-            if (j == 0) {
-                m = m_new;
-            } else {
-                const bool grow = m_new > m + kGrow;
-                if (__any_sync(0xffffffffu, grow)) {
-                    const float f = grow ? exp2_approx(m - m_new) : 1.0f;
-                    if (grow) m = m_new;
-                    const unsigned long long f2 = pack2(f, f);
-                    l2 = fma2(l2, f2, 0ull);
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32w(col_o + 32 * c, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_st32w(col_o + 32 * c, o);
-                    }
-                }
-            }
-            const float neg = m == -INFINITY ? 0.f : -m;
-            const unsigned long long neg2 = pack2(neg, neg);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t p[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const unsigned long long y =
-                        fma2(pack2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, neg2);
-                    const float p0 = exp2_approx(__uint_as_float((unsigned)y));
-                    const float p1 = exp2_approx(__uint_as_float((unsigned)(y >> 32)));
-                    l2 = add2(l2, pack2(p0, p1));
-                    p[e >> 1] = pack_bf16x2(p0, p1);
-                }
-                tmem_st16w(col_s + 16 * c, p);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.p_full[i]);
-        }
-        if (n_own > 0 && ok && wait_phase(&S.o_full[i], 0, err, status) &&
-            wait_phase(&S.v_clean[0], 0, err, status) &&
-            wait_phase(&S.v_clean[n_kv - 1 - j_mask], 0, err, status)) {
-            tc_fence_after();
-            const float l = __uint_as_float((unsigned)l2) + __uint_as_float((unsigned)(l2 >> 32));
-            const float inv = 1.0f / l;
-            const bool bad = *(volatile int*)&S.any_bad != 0;
-            uint8_t* stage = reinterpret_cast<uint8_t*>(S.q[i][0]);   // every S of the tile is done: its queries are free
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32w(col_o + 32 * c, o);
+                for (int c = 0; c < 4; ++c) tmem_ld32w(col_s + 32 * c, v[c]);
                 tmem_ld_wait();
-                float f[32];
+                if (j >= j_own) {
+                    const int lim = tok - j * kKeys;       // keys up to lim are seen
 #pragma unroll
-                for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
-                if (bad) {
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int d = 32 * c + e;
-                        const bool up = S.bad[kPosInf][d] <= tok, dn = S.bad[kNegInf][d] <= tok;
-                        if (S.bad[kNan][d] <= tok || (up && dn)) f[e] = __uint_as_float(0x7FC00000u);
-                        else if (up) f[e] += INFINITY;
-                        else if (dn) f[e] -= INFINITY;
-                    }
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e > lim) v[c][e] = 0xFF800000u;
                 }
+                float mx[4];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    const int ch = 4 * c + (e >> 3);
-                    uint4 w;
-                    w.x = pack_bf16x2(f[e], f[e + 1]);
-                    w.y = pack_bf16x2(f[e + 2], f[e + 3]);
-                    w.z = pack_bf16x2(f[e + 4], f[e + 5]);
-                    w.w = pack_bf16x2(f[e + 6], f[e + 7]);
-                    *reinterpret_cast<uint4*>(stage + row * 256 + ((ch ^ (row & 15)) << 4)) = w;
+                for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(v[c][0]);
+                // a NaN logit makes the maximum NaN, and with it the whole row; so does +inf (inf - inf)
+                auto take_max = [&](int c, int e) {
+                    if (e + 2 < 32) mx[c] = max3_nan(mx[c], __uint_as_float(v[c][e + 1]), __uint_as_float(v[c][e + 2]));
+                    else mx[c] = max3_nan(mx[c], __uint_as_float(v[c][e + 1]), mx[c]);
+                };
+                // quarter c of P into TMEM, its sum into l.  `poly`: part of the exponentials on the
+                // FMA pipes (not where logits are masked: -inf must give an exact 0 there);
+                // `with_max`: also takes the maxima
+                unsigned long long neg2;
+                auto exponentials = [&](int c, unsigned long long& l, auto poly, auto with_max) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const unsigned long long y =
+                            fma2(pack2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, neg2);
+                        float p0, p1;
+                        if (poly.value && e / 2 % kPolyEvery == kPolyEvery - 1) {
+                            exp2_poly2(y, p0, p1);
+                        } else {
+                            p0 = exp2_approx(__uint_as_float((unsigned)y));
+                            p1 = exp2_approx(__uint_as_float((unsigned)(y >> 32)));
+                        }
+                        if (with_max.value) {
+                            take_max(c, e);
+                            if (c == 1) take_max(3, e);
+                        }
+                        l = add2(l, pack2(p0, p1));
+                        p[e >> 1] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st16w(col_s + 16 * c, p);
+                };
+                auto arrive = [&](int part) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S.p_full[i][part]);
+                };
+                auto set_neg = [&]() {
+                    const float neg = m == -INFINITY ? 0.f : -m;
+                    neg2 = pack2(neg, neg);
+                };
+                auto step = [&](auto poly) {
+                    unsigned long long l = l2;
+                    set_neg();
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < kEarly; ++c) exponentials(c, l, poly, std::true_type());
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) take_max(c, e);
+                    }
+                    float m_new = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
+                    if (m_new == INFINITY) m_new = __uint_as_float(0x7FC00000u);
+                    const bool grow = !(m_new <= m + kGrow);
+                    if (j == 0 || __any_sync(0xffffffffu, grow)) {
+                        // once more from the new maximum; nothing has been handed on yet
+                        const float f = grow ? exp2_approx(m - m_new) : 1.0f;
+                        if (grow || j == 0) m = m_new;
+                        set_neg();
+                        if (j > 0) {
+                            l2 = fma2(l2, pack2(f, f), 0ull);
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t o[32];
+                                tmem_ld32w(col_o + 32 * c, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st32w(col_o + 32 * c, o);
+                            }
+                        }
+                        l = l2;
+#pragma unroll
+                        for (int c = 0; c < kEarly; ++c) exponentials(c, l, poly, std::false_type());
+                    }
+                    arrive(0);
+#pragma unroll
+                    for (int c = kEarly; c < 4; ++c) exponentials(c, l, poly, std::false_type());
+                    l2 = l;
+                    arrive(1);
+                };
+                if (j < j_own) step(std::true_type());
+                else step(std::false_type());
+            }
+            if (!ok) break;
+            if (n_own > 0) {
+                const int g = n_mask - 1;                  // the item's last guarded tile: all of `bad` is there
+                if (!(ok = wait_phase(&S.o_full[i], n_o & 1, err, status) &&
+                           wait_phase(&S.v_clean[g % kGuards], (g / kGuards) & 1, err, status)))
+                    break;
+                ++n_o;
+                tc_fence_after();
+                const float l = __uint_as_float((unsigned)l2) + __uint_as_float((unsigned)(l2 >> 32));
+                const float inv = 1.0f / l;
+                const bool bad = *(volatile int*)&S.any_bad != 0;
+                const bool live = row < ta * G && tok < it.len;
+                char* dst = reinterpret_cast<char*>(
+                    out + ((int64_t)(it.tok0 + tok) * n_q_heads + it.head * G + row_head) * kHeadDim);
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32w(col_o + 32 * c, o);
+                    tmem_ld_wait();
+                    float f[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
+                    if (bad) {
+#pragma unroll 1
+                        for (int e = 0; e < 32; ++e) {
+                            const int d = 32 * c + e;
+                            const bool up = S.bad[kPosInf][d] <= tok, dn = S.bad[kNegInf][d] <= tok;
+                            const float add = S.bad[kNan][d] <= tok || (up && dn) ? __uint_as_float(0x7FC00000u)
+                                              : up ? INFINITY : dn ? -INFINITY : 0.f;
+#pragma unroll
+                            for (int u = 0; u < 32; ++u) f[u] += u == e ? add : 0.f;
+                        }
+                    }
+                    if (live) {
+                        uint32_t w[2][8];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) w[e >> 4][(e >> 1) & 7] = pack_bf16x2(f[e], f[e + 1]);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (wide) {
+                                store_32b(dst + 64 * c + 32 * h, w[h]);
+                            } else {
+                                uint4* d4 = reinterpret_cast<uint4*>(dst + 64 * c + 32 * h);
+                                d4[0] = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
+                                d4[1] = make_uint4(w[h][4], w[h][5], w[h][6], w[h][7]);
+                            }
+                        }
+                    }
                 }
             }
             __syncwarp();
-            // two rows per instruction, 256 contiguous bytes each
-            for (int r = 0; r < 32; r += 2) {
-                const int rr = quarter * 32 + r + (lane >> 4), ch = lane & 15;
-                const int t = first + rr / G;
-                if (rr < ta * G && t < len) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 256 + ((ch ^ (rr & 15)) << 4));
-                    uint4* dst = reinterpret_cast<uint4*>(out) +
-                                 (((int64_t)tok0 + t) * n_q_heads + head * G + rr % G) * (kHeadDim / 8) + ch;
-                    *dst = w;
-                }
-            }
+            if (lane == 0) mbar_arrive(&S.item_done);
         }
     }
     tc_fence_before();
@@ -460,28 +687,36 @@ cudaError_t launch_prompt_attn(const qsa_dims& d, const void* q, int64_t q_ld, c
     auto encode = encode_fn();
     if (!encode) return cudaErrorNotSupported;
     const int G = d.n_q_heads / d.n_kv_heads;
-    const int ta = kRows / G;
-    auto map = [&](CUtensorMap* t, const void* p, int heads, int64_t ld, int box_heads, int box_tok) {
-        const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)heads, (cuuint64_t)n_tok};
-        const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)ld * 2};
-        const cuuint32_t box[3] = {64u, (cuuint32_t)box_heads, (cuuint32_t)box_tok};
-        const cuuint32_t estr[3] = {1u, 1u, 1u};
-        return encode(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+    const cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    CUtensorMap tq, tk, tv;
+    {
+        // queries [token][head][128]: a box is 64 dims of G heads of one tile's tokens
+        const cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)d.n_q_heads, (cuuint64_t)n_tok};
+        const cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)q_ld * 2};
+        const cuuint32_t box[3] = {64u, (cuuint32_t)G, (cuuint32_t)(kRows / G)};
+        if (encode(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    auto kv_map = [&](CUtensorMap* t, const void* p, int64_t ld) {
+        // K or V as (dim of a half, token, half, head): a box is both 64-dim halves of 128 tokens
+        const cuuint64_t dims[4] = {64u, (cuuint64_t)n_tok, 2u, (cuuint64_t)d.n_kv_heads};
+        const cuuint64_t strides[3] = {(cuuint64_t)ld * 2, 128u, (cuuint64_t)kHeadDim * 2};
+        const cuuint32_t box[4] = {64u, (cuuint32_t)kKeys, 2u, 1u};
+        return encode(t, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p), dims, strides, box, estr,
                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
-    CUtensorMap tq, tk, tv;
-    if (!map(&tq, q, d.n_q_heads, q_ld, G, ta) || !map(&tk, k, d.n_kv_heads, k_ld, 1, kKeys) ||
-        !map(&tv, v, d.n_kv_heads, v_ld, 1, kKeys))
-        return cudaErrorInvalidValue;
+    if (!kv_map(&tk, k, k_ld) || !kv_map(&tv, v, v_ld)) return cudaErrorInvalidValue;
     static std::atomic<bool> attr[128];
     const int smem = (int)sizeof(PromptSmem) + 1024;
     if (!set_smem_once((const void*)k_prompt_attn, smem, attr)) return cudaErrorInvalidValue;
     const int64_t ctas = prompt_attn_ctas(d, n_tok);
     const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / sqrtf((float)d.head_dim);
     k_prompt_attn<<<(unsigned)ctas, kThreads, smem, st>>>(
-        tq, tk, tv, cu_len, d.batch, n_tok, d.n_q_heads, d.n_kv_heads, ctas / d.n_kv_heads, scale * 1.4426950408889634f,
-        (__nv_bfloat16*)out, status);
+        tq, tk, tv, cu_len, d.batch, n_tok, d.n_q_heads, d.n_kv_heads, (int)(ctas / d.n_kv_heads),
+        scale * 1.4426950408889634f, (__nv_bfloat16*)out, status);
     return cudaGetLastError();
 }
 
