@@ -15,9 +15,8 @@
 // One pass over the keys with a running maximum m and sum l (exp2 domain):
 //     S = Q K^T;  P = exp2(scale log2(e) S - m);  l = l f + sum P;  O = O f + P V.
 // m only moves when a row's maximum grew by more than 8 (a factor of 256 in P, which
-// fp32 sums and bf16 P carry without loss), so the factor f is 1 in almost every step:
-// the exponentials start from the old m while the new maximum is still being taken, and
-// O, which lies in TMEM, is read and written back only where m moved.
+// fp32 sums and bf16 P carry without loss), so the factor f is 1 in almost every step, and
+// O, which lies in TMEM, is read and written back only in the others.
 //
 // The grid has one CTA per item, but a CTA that finishes an item takes the next one off
 // the queue of CTAs that have not started (cluster launch control): barriers and TMEM are
@@ -43,7 +42,6 @@
 
 #include <atomic>
 #include <climits>
-#include <type_traits>
 
 #include "sm100_host.cuh"
 #include "sm100_ptx.cuh"
@@ -66,9 +64,7 @@ constexpr uint32_t kTileBytes = kKeys * kHeadDim * 2;
 constexpr uint32_t kTmemColsPrompt = 512;
 constexpr uint32_t kColO = 256;           // TMEM column of O of tile A (S of A, S of B before it)
 constexpr float kGrow = 8.0f;             // growth of a row maximum (log2) that rescales O
-constexpr int kPolyEvery = 4;             // one pair of exponentials in this many goes to the FMA pipes
 constexpr int kEarly = 3;                 // quarters of P that the MMA may read before the last one is there
-static_assert(kEarly == 3, "the maxima of quarter 3 are taken with those of quarter 1");
 
 enum { kPosInf = 0, kNegInf = 1, kNan = 2 };
 
@@ -111,34 +107,6 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
 {
     unsigned long long d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// 2^x of two values on the FMA pipes: x = n + f with n the nearest integer (by adding and
-// taking away 1.5 * 2^23), 2^f a cubic with p(0) = 1 whose largest relative error on
-// [-1/2, 1/2] is as small as a cubic's can be (least squares reweighted to it: 2^-13.2, a
-// sixteenth of P's bf16 rounding), 2^n by adding n to the exponent.  x below -127 counts as
-// -127, which gives 0; x must not be NaN and stay below 128.
-__device__ __forceinline__ void exp2_poly2(unsigned long long x2, float& p0, float& p1)
-{
-    constexpr float kMagic = 12582912.0f;
-    const float x0 = fmaxf(__uint_as_float((unsigned)x2), -127.0f);
-    const float x1 = fmaxf(__uint_as_float((unsigned)(x2 >> 32)), -127.0f);
-    const unsigned long long x = pack2(x0, x1);
-    const unsigned long long t = add2(x, pack2(kMagic, kMagic));
-    const unsigned long long n = add2(t, pack2(-kMagic, -kMagic));
-    const unsigned long long f = fma2(n, pack2(-1.0f, -1.0f), x);
-    unsigned long long p = fma2(f, pack2(0.05500893f, 0.05500893f), pack2(0.24221097f, 0.24221097f));
-    p = fma2(p, f, pack2(0.6932829f, 0.6932829f));
-    p = fma2(p, f, pack2(1.0f, 1.0f));
-    p0 = __uint_as_float((unsigned)p + ((unsigned)t << 23));
-    p1 = __uint_as_float((unsigned)(p >> 32) + ((unsigned)(t >> 32) << 23));
-}
-
-__device__ __forceinline__ float max3_nan(float a, float b, float c)
-{
-    float d;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 
@@ -490,6 +458,8 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const int quarter = warp & 3;
         const int row = quarter * 32 + lane;
         const int row_tok = row / G, row_head = row % G;   // rows past ta * G hold nothing and are not stored
+        // tokens (from tile A's first) of the warp's first and last row
+        const int warp_lo = i * ta + quarter * 32 / G, warp_hi = i * ta + (quarter * 32 + 31) / G;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t col_s = lanes + i * kKeys, col_o = lanes + kColO + i * kHeadDim;
         const unsigned long long sc2 = pack2(scale_log2, scale_log2);
@@ -513,102 +483,77 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32w(col_s + 32 * c, v[c]);
                 tmem_ld_wait();
+                // quarters from n_seen on are masked for the whole warp, quarters that end at or below
+                // its first row's token for none of its rows; in between by element
+                int n_seen = 4;
                 if (j >= j_own) {
                     const int lim = tok - j * kKeys;       // keys up to lim are seen
+                    const int lo = warp_lo + (it.t0 - j * kKeys), hi = warp_hi + (it.t0 - j * kKeys);
+                    n_seen = min(4, hi < 0 ? 0 : hi / 32 + 1);
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
+                        if (32 * c + 31 > lo) {
+                            const int k = lim - 32 * c;
+                            const uint32_t seen = k >= 31 ? 0xFFFFFFFFu : k < 0 ? 0u : (2u << k) - 1u;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (32 * c + e > lim) v[c][e] = 0xFF800000u;
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1u)) v[c][e] = 0xFF800000u;
+                        }
                 }
                 float mx[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(v[c][0]);
-                // a NaN logit makes the maximum NaN, and with it the whole row; so does +inf (inf - inf)
-                auto take_max = [&](int c, int e) {
-                    if (e + 2 < 32) mx[c] = max3_nan(mx[c], __uint_as_float(v[c][e + 1]), __uint_as_float(v[c][e + 2]));
-                    else mx[c] = max3_nan(mx[c], __uint_as_float(v[c][e + 1]), mx[c]);
-                };
-                // quarter c of P into TMEM, its sum into l.  `poly`: part of the exponentials on the
-                // FMA pipes (not where logits are masked: -inf must give an exact 0 there);
-                // `with_max`: also takes the maxima
-                unsigned long long neg2;
-                auto exponentials = [&](int c, unsigned long long& l, auto poly, auto with_max) {
-                    uint32_t p[16];
+                for (int c = 0; c < 4; ++c) {
+                    mx[c] = fmaxf(__uint_as_float(v[c][0]), __uint_as_float(v[c][1]));
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const unsigned long long y =
-                            fma2(pack2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, neg2);
-                        float p0, p1;
-                        if (poly.value && e / 2 % kPolyEvery == kPolyEvery - 1) {
-                            exp2_poly2(y, p0, p1);
-                        } else {
-                            p0 = exp2_approx(__uint_as_float((unsigned)y));
-                            p1 = exp2_approx(__uint_as_float((unsigned)(y >> 32)));
-                        }
-                        if (with_max.value) {
-                            take_max(c, e);
-                            if (c == 1) take_max(3, e);
-                        }
-                        l = add2(l, pack2(p0, p1));
-                        p[e >> 1] = pack_bf16x2(p0, p1);
+                    for (int e = 2; e < 32; e += 2)
+                        mx[c] = max3(mx[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+                }
+                const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale_log2;
+                const bool grow = m_new > m + kGrow;
+                if (j == 0) {
+                    m = m_new;
+                } else if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? exp2_approx(m - m_new) : 1.0f;
+                    if (grow) m = m_new;
+                    l2 = fma2(l2, pack2(f, f), 0ull);
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32w(col_o + 32 * c, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st32w(col_o + 32 * c, o);
                     }
-                    tmem_st16w(col_s + 16 * c, p);
-                };
-                auto arrive = [&](int part) {
-                    tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&S.p_full[i][part]);
-                };
-                auto set_neg = [&]() {
-                    const float neg = m == -INFINITY ? 0.f : -m;
-                    neg2 = pack2(neg, neg);
-                };
-                auto step = [&](auto poly) {
-                    unsigned long long l = l2;
-                    set_neg();
-                    if (j > 0) {
+                }
+                const float neg = m == -INFINITY ? 0.f : -m;
+                const unsigned long long neg2 = pack2(neg, neg);
 #pragma unroll
-                        for (int c = 0; c < kEarly; ++c) exponentials(c, l, poly, std::true_type());
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+                    if (c < n_seen) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const unsigned long long y =
+                                fma2(pack2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1])), sc2, neg2);
+                            const float p0 = exp2_approx(__uint_as_float((unsigned)y));
+                            const float p1 = exp2_approx(__uint_as_float((unsigned)(y >> 32)));
+                            l2 = add2(l2, pack2(p0, p1));
+                            p[e >> 1] = pack_bf16x2(p0, p1);
+                        }
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 32; e += 2) take_max(c, e);
+                        for (int e = 0; e < 16; ++e) p[e] = 0u;
                     }
-                    float m_new = max3_nan(max3_nan(mx[0], mx[1], mx[2]), mx[3], mx[3]) * scale_log2;
-                    if (m_new == INFINITY) m_new = __uint_as_float(0x7FC00000u);
-                    const bool grow = !(m_new <= m + kGrow);
-                    if (j == 0 || __any_sync(0xffffffffu, grow)) {
-                        // once more from the new maximum; nothing has been handed on yet
-                        const float f = grow ? exp2_approx(m - m_new) : 1.0f;
-                        if (grow || j == 0) m = m_new;
-                        set_neg();
-                        if (j > 0) {
-                            l2 = fma2(l2, pack2(f, f), 0ull);
-#pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t o[32];
-                                tmem_ld32w(col_o + 32 * c, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                                tmem_st32w(col_o + 32 * c, o);
-                            }
-                        }
-                        l = l2;
-#pragma unroll
-                        for (int c = 0; c < kEarly; ++c) exponentials(c, l, poly, std::false_type());
+                    tmem_st16w(col_s + 16 * c, p);
+                    if (c == kEarly - 1 || c == 3) {
+                        const int part = c == 3;
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&S.p_full[i][part]);
                     }
-                    arrive(0);
-#pragma unroll
-                    for (int c = kEarly; c < 4; ++c) exponentials(c, l, poly, std::false_type());
-                    l2 = l;
-                    arrive(1);
-                };
-                if (j < j_own) step(std::true_type());
-                else step(std::false_type());
+                }
             }
             if (!ok) break;
             if (n_own > 0) {
@@ -624,38 +569,39 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 const bool live = row < ta * G && tok < it.len;
                 char* dst = reinterpret_cast<char*>(
                     out + ((int64_t)(it.tok0 + tok) * n_q_heads + it.head * G + row_head) * kHeadDim);
-#pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32w(col_o + 32 * c, o);
-                    tmem_ld_wait();
-                    float f[32];
+                uint32_t o[4][32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(o[e]) * inv;
-                    if (bad) {
-#pragma unroll 1
-                        for (int e = 0; e < 32; ++e) {
-                            const int d = 32 * c + e;
-                            const bool up = S.bad[kPosInf][d] <= tok, dn = S.bad[kNegInf][d] <= tok;
-                            const float add = S.bad[kNan][d] <= tok || (up && dn) ? __uint_as_float(0x7FC00000u)
-                                              : up ? INFINITY : dn ? -INFINITY : 0.f;
+                for (int c = 0; c < 4; ++c) tmem_ld32w(col_o + 32 * c, o[c]);
+                tmem_ld_wait();
 #pragma unroll
-                            for (int u = 0; u < 32; ++u) f[u] += u == e ? add : 0.f;
-                        }
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[c][e] = __float_as_uint(__uint_as_float(o[c][e]) * inv);
+                if (bad) {
+#pragma unroll 1
+                    for (int d = 0; d < kHeadDim; ++d) {
+                        const bool up = S.bad[kPosInf][d] <= tok, dn = S.bad[kNegInf][d] <= tok;
+                        const float add = S.bad[kNan][d] <= tok || (up && dn) ? __uint_as_float(0x7FC00000u)
+                                          : up ? INFINITY : dn ? -INFINITY : 0.f;
+#pragma unroll
+                        for (int u = 0; u < kHeadDim; ++u)
+                            if (u == d) o[u / 32][u % 32] = __float_as_uint(__uint_as_float(o[u / 32][u % 32]) + add);
                     }
-                    if (live) {
-                        uint32_t w[2][8];
+                }
+                if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) w[e >> 4][(e >> 1) & 7] = pack_bf16x2(f[e], f[e + 1]);
+                    for (int c = 0; c < 8; ++c) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (wide) {
-                                store_32b(dst + 64 * c + 32 * h, w[h]);
-                            } else {
-                                uint4* d4 = reinterpret_cast<uint4*>(dst + 64 * c + 32 * h);
-                                d4[0] = make_uint4(w[h][0], w[h][1], w[h][2], w[h][3]);
-                                d4[1] = make_uint4(w[h][4], w[h][5], w[h][6], w[h][7]);
-                            }
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(o[c / 2][16 * (c % 2) + 2 * e]),
+                                               __uint_as_float(o[c / 2][16 * (c % 2) + 2 * e + 1]));
+                        if (wide) {
+                            store_32b(dst + 32 * c, w);
+                        } else {
+                            uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
+                            d4[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            d4[1] = make_uint4(w[4], w[5], w[6], w[7]);
                         }
                     }
                 }
