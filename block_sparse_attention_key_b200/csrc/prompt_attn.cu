@@ -144,6 +144,49 @@ __device__ __forceinline__ void store_32b(void* p, const uint32_t (&w)[8])
                  : "memory");
 }
 
+// Item of grid index `cta` (index / KV heads is its place among the query tile pairs), by one
+// warp; len 0 if there is none or its sequence's bounds are malformed.  Long items first:
+// CTAs take them in the order of the grid, and one that starts last ends alone.
+__device__ __forceinline__ Item find_item(const int32_t* __restrict__ cu, int batch, int n_tok, int n_tiles, int tq,
+                                          int n_kv_heads, int cta, int lane)
+{
+    const int y = cta / n_kv_heads, head = cta % n_kv_heads;
+    int s = -1, tile = 0;
+    if (batch <= 32) {
+        // every sequence in a lane: by tile number from the highest on, all sequences that have it
+        int n = 0;
+        if (lane < batch) {
+            const int a = __ldg(cu + lane), b = __ldg(cu + lane + 1);
+            if (a >= 0 && a <= b && b <= n_tok) n = (int)(((int64_t)(b - a) + tq - 1) / tq);
+        }
+        // tiles of number t or higher; the item's number is the largest t with more than y of them
+        auto at_least = [&](int t) { return (int)__reduce_add_sync(0xffffffffu, n > t ? n - t : 0); };
+        int lo = 0, hi = __reduce_max_sync(0xffffffffu, n);
+        if (y < at_least(0)) {
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                (at_least(mid) > y ? lo : hi) = mid;
+            }
+            tile = lo;
+            const int nth = y - at_least(tile + 1);
+            const unsigned has = __ballot_sync(0xffffffffu, n > tile);
+            const unsigned mine = __ballot_sync(0xffffffffu, n > tile && __popc(has & ((1u << lane) - 1u)) == nth);
+            s = __ffs(mine) - 1;
+        }
+    } else {
+        // by place, from the last on.  Sequence s's tiles start at index cu[s] / tq + s, which
+        // leaves every sequence at least ceil(len / tq) indices and needs no prefix sum
+        const int x = n_tiles - 1 - y;
+        s = find_sequence(batch, lane, [&](int i) { return __ldg(cu + i) / tq + i <= x; });
+        if (s >= 0) tile = x - (__ldg(cu + s) / tq + s);
+    }
+    if (s < 0) return Item{0, 0, 0, head};
+    const int a = __ldg(cu + s), b = __ldg(cu + s + 1);
+    const int64_t first = (int64_t)tile * tq;
+    if (a < 0 || a > b || b > n_tok || first < 0 || first >= b - a) return Item{0, 0, 0, head};
+    return Item{b - a, a, (int)first, head};
+}
+
 }  // namespace
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -159,10 +202,14 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     const int ta = kRows / G;                              // tokens of a query tile
     const int tq = 2 * ta;
 
-    if (warp == 0 && lane == 0) {
-        prefetch_tensormap(&tmap_q);
-        prefetch_tensormap(&tmap_k);
-        prefetch_tensormap(&tmap_v);
+    Item it0{0, 0, 0, 0};
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_tensormap(&tmap_q);
+            prefetch_tensormap(&tmap_k);
+            prefetch_tensormap(&tmap_v);
+        }
+        it0 = find_item(cu_len, batch, n_tok, n_tiles, tq, n_kv_heads, blockIdx.x, lane);
     }
     if (warp == 1) {
         tmem_alloc(&S.tmem_base, kTmemColsPrompt);
@@ -231,6 +278,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
         if (warp == 0) {
             // ---------------- items and loads ----------------
+            Item it = it0;
             int cta = blockIdx.x, k_ring = 0, n_mask = 0, asked = 0, n_item = 0;
             bool ok = true, more = true;
             while (ok && more) {
@@ -245,17 +293,6 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     }
                 }
                 ++asked;
-                // the longest rows of each sequence first.  Sequence s's tiles start at index
-                // cu[s] / tq + s, which leaves every sequence at least ceil(len / tq) indices
-                // and needs no prefix sum
-                const int x = n_tiles - 1 - cta / n_kv_heads;
-                const int s = find_sequence(batch, lane, [&](int i) { return __ldg(cu_len + i) / tq + i <= x; });
-                Item it{0, 0, 0, cta % n_kv_heads};
-                if (s >= 0) {
-                    const int a = __ldg(cu_len + s), b = __ldg(cu_len + s + 1);
-                    const int64_t first = (int64_t)(x - (a / tq + s)) * tq;
-                    if (a >= 0 && a <= b && b <= n_tok && first >= 0 && first < b - a) it = Item{b - a, a, (int)first, it.head};
-                }
                 if (it.len > 0) {
                     const int slot = n_item % kItems;
                     if (n_item >= kItems && !wait_phase(&S.item_empty[slot], ((n_item / kItems) - 1) & 1, err, status)) break;
@@ -272,7 +309,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                                 tma_load_3d(S.q[i][h], &tmap_q, &S.q_full[i], 64 * h, it.head * G, it.tok0 + it.t0 + i * ta);
                             return true;
                         };
-                        ok = load_q(0);
+                        // the first K and V ahead of the queries, whose buffers the last item still reads
                         for (int k = 0; k < 2 * t.n_kv && ok; ++k) {
                             const int ring = k_ring % kRing;
                             if (k_ring >= kRing && !(ok = wait_phase(&S.kv_empty[ring], ((k_ring / kRing) - 1) & 1, err, status)))
@@ -285,7 +322,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                             mbar_arrive_expect_tx(bar, kTileBytes);
                             tma_load_4d(S.kv[ring], (k & 1) ? &tmap_v : &tmap_k, bar, 0, it.tok0 + (k >> 1) * kKeys, 0, it.head);
                             ++k_ring;
-                            if (k == 0) ok = load_q(1);    // also for an absent B: its barriers keep step with A's
+                            if (k == 1) ok = load_q(0) && load_q(1);   // also for an absent B: its barriers keep step with A's
                         }
                     }
                     ++n_item;
@@ -296,6 +333,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 fence_proxy_async();                       // read before the next answer overwrites it
                 __syncwarp();
                 more = cta >= 0;
+                if (more) it = find_item(cu_len, batch, n_tok, n_tiles, tq, n_kv_heads, cta, lane);
             }
             if (ok) {
                 const int slot = n_item % kItems;
