@@ -10,19 +10,25 @@
 // after a per-row power of two brings their largest magnitude to [2^14, 2^15) (a bf16
 // value then keeps every bit down to 2^-31 of the row's largest, and errs by 2^-39 of it
 // below); the power is undone in the logits' fp32 scale.  Probabilities are rounded to
-// fp16 times 2^14 (11 bits; those below 2^-28 of the running maximum lose bits one by
+// fp16 times 2^13 (11 bits; those below 2^-27 of the running maximum lose bits one by
 // one), the sum keeps the unrounded ones.  fp32 accumulation throughout.
 //
-// Work unit, splits and pipeline: one CTA per (split, KV head, draft group), its rows the
-// group's query heads of that KV head (<= 32), tokens on the M side of mma.sync m16n8k16.
-// The splits of a (group, KV head) form one thread-block cluster and merge in its first
-// CTA's shared memory, so a call needs no scratch.  What differs from a bf16 gather is
-// that unpacking, not the copies, is the work: operands never pass through shared memory
-// unpacked.  The contraction's order is free, so a lane takes 32 consecutive dims of its
-// K rows (one 16-byte shared load = all A fragments of a row, the query fragments use the
-// same order), and 16 consecutive dims of its four V tokens (8 bytes and one scale each);
-// V pairs are two tokens of one dim: their nibbles are interleaved with bit selects
-// before the conversion (4 logic operations per 16 values).
+// Work unit and splits: one CTA per (split, KV head, draft group), its rows the group's
+// query heads of that KV head (<= 32), tokens on the M side of mma.sync m16n8k16.  The
+// splits of a (group, KV head) form one thread-block cluster and merge in its first CTA's
+// shared memory, so a call needs no scratch.  What differs from a bf16 gather is that
+// unpacking, not the copies, is the work (about 500 instructions per warp and 32 tokens,
+// 2.3 KB of each K and V), so operands never pass through shared memory unpacked and
+// warps do not wait for one another: each takes 32 tokens at a time through a ring of its
+// own (cp.async, four lanes per row of codes), and only the end is a block's.
+//
+// The contraction's order is free, so a lane takes 32 consecutive dims of its K rows (one
+// 16-byte shared load = all A fragments of a row, the query fragments use the same order),
+// and 16 consecutive dims of its V tokens (8 bytes and one scale each); V pairs are two
+// tokens of one dim: their nibbles are interleaved with bit selects before the conversion
+// (4 logic operations per 16 values).  The running maximum moves when it grew by more
+// than 2 (probabilities then reach 2^16 / 2, inside fp16), so accumulators are rescaled
+// in few steps.
 //
 // Masked places: absent tokens are zero-filled and their logits -inf.  A scale may be NaN
 // (the append writes that for values that are not finite): a draft's tail token that is
@@ -31,7 +37,6 @@
 
 #include <atomic>
 #include <climits>
-#include <mutex>
 
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
@@ -42,28 +47,29 @@ namespace qsa {
 
 namespace {
 
-constexpr int kTok4 = 64;                      // tokens per stage
+constexpr int kTok4 = 32;                      // tokens a warp takes at a time
 constexpr int kCodeRow = kHeadDim / 2;         // 64 B of codes per token row
 constexpr int kScaleRow = kHeadDim / 16;       // 8 B of scales per token row
-constexpr int kCodes = kTok4 * kCodeRow;       // 4 KiB of K (or V) codes per stage
+constexpr int kCodes = kTok4 * kCodeRow;       // 2 KiB of K (or V) codes
 constexpr int kScales = kTok4 * kScaleRow;
-constexpr int kStage4 = 2 * (kCodes + kScales);  // K codes, V codes, K scales, V scales
+constexpr int kTile4 = 2 * (kCodes + kScales); // K codes, V codes, K scales, V scales
 constexpr int kItems4 = kSelCap + 2;           // selected blocks + up to 2 tail blocks
-constexpr int kItemCap4 = 592;                 // items of one split, in whole stages
-constexpr int kMaxStages4 = 16;
+constexpr int kItemCap4 = 576;                 // items of one split, in whole tiles
 constexpr int kMaxSplits4 = 16;                // one cluster
-constexpr float kProbShift = 14.0f;            // probabilities are held times 2^14
+constexpr float kProbShift = 13.0f;            // probabilities are held times 2^13
+constexpr float kGrow4 = 2.0f;                 // growth of a row maximum (log2) that rescales the sums
 
 struct Layout4 {
-    int q, stage, tok, ioff, ipos, rowt, rows, total;
+    int q, ring, tok, ioff, ipos, rowt, rows, total;
 };
-__host__ __device__ inline Layout4 layout4(int rp, int stages)
+// `area`: bytes of the warps' rings, which the merges use at the end
+__host__ __device__ inline Layout4 layout4(int rp, int warps, int depth, int area)
 {
     Layout4 L;
     L.q = 0;
-    L.stage = rp * kHeadDim * 2;
-    L.tok = L.stage + stages * kStage4;
-    L.ioff = L.tok + stages * kTok4 * 4;
+    L.ring = rp * kHeadDim * 2;
+    L.tok = L.ring + area;
+    L.ioff = L.tok + warps * depth * kTok4 * 4;
     L.ipos = L.ioff + kItemCap4 * 8;
     L.rowt = L.ipos + kItemCap4 * 4;
     L.rows = L.rowt + 32 * 4;
@@ -85,16 +91,11 @@ __device__ __forceinline__ void cp_async8(uint32_t saddr, const void* g, int src
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(saddr), "l"(g), "r"(src_bytes));
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::); }
-__device__ __forceinline__ void cp_wait_pending(int n)
+__device__ __forceinline__ float exp2_approx(float x)
 {
-    // wait until at most n committed groups are still in flight (n < kMaxStages4)
-    switch (n) {
-#define QSA_WAIT(i) case i: asm volatile("cp.async.wait_group " #i ";\n" ::); break
-    QSA_WAIT(0); QSA_WAIT(1); QSA_WAIT(2); QSA_WAIT(3); QSA_WAIT(4); QSA_WAIT(5); QSA_WAIT(6); QSA_WAIT(7);
-    QSA_WAIT(8); QSA_WAIT(9); QSA_WAIT(10); QSA_WAIT(11); QSA_WAIT(12); QSA_WAIT(13); QSA_WAIT(14);
-#undef QSA_WAIT
-    default: asm volatile("cp.async.wait_group 15;\n" ::); break;
-    }
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a)
@@ -178,28 +179,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 
 }  // namespace
 
-// NT = 8-row column tiles of the MMA's N side (rows = drafts x G <= 8 * NT); NWG = groups
-// of 4 compute warps, each group taking every NWG-th stage with its own softmax state.
-template <int NT, int NWG>
-__global__ void __launch_bounds__(128 * NWG)
+// NT = 8-row column tiles of the MMA's N side (rows = drafts x G <= 8 * NT); KW = warps;
+// D = tiles in flight per warp.
+template <int NT, int KW, int D>
+__global__ void __launch_bounds__(32 * KW)
 k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_codes,
                   const uint8_t* __restrict__ k_scales, const uint8_t* __restrict__ v_codes,
                   const uint8_t* __restrict__ v_scales, const int32_t* __restrict__ q_seq,
                   const int32_t* __restrict__ q_pos, const int32_t* __restrict__ sel_idx,
                   const int32_t* __restrict__ sel_cnt, const int32_t* __restrict__ page_table, int page_tokens,
                   int64_t table_ld, int64_t n_pages, int batch, int n_q_heads, int n_kv_heads, int64_t kv_capacity,
-                  int bs_log2, int top_k, int group_q, float scale_log2, int items_per_split, int n_split,
-                  int n_stages, __nv_bfloat16* __restrict__ out, unsigned* status)
+                  int bs_log2, int top_k, int group_q, float scale_log2, int items_per_split, int n_split, int area,
+                  __nv_bfloat16* __restrict__ out, unsigned* status)
 {
     constexpr int RP = 8 * NT;           // padded rows
-    constexpr int kT = 128 * NWG;        // threads
-    constexpr int kW = 4 * NWG;          // warps
+    constexpr int kT = 32 * KW;          // threads
     constexpr int kPerT = (kItemCap4 + kT - 1) / kT;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int s_cnt, s_nitems, s_seq, s_nc0, s_tlast;
-    const Layout4 SL = layout4(RP, n_stages);
+    const Layout4 SL = layout4(RP, KW, D, area);
     const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
-    int* s_tok = reinterpret_cast<int*>(smem + SL.tok);
     long long* s_ioff = reinterpret_cast<long long*>(smem + SL.ioff);
     int* s_ipos = reinterpret_cast<int*>(smem + SL.ipos);
     int* s_rowt = reinterpret_cast<int*>(smem + SL.rowt);
@@ -213,7 +212,7 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     const int R = group_q * G;
     const int64_t qi0 = (int64_t)grp * group_q;
     const int bs = 1 << bs_log2;     // tokens per block
-    const int ipt = kTok4 >> bs_log2;  // blocks per stage
+    const int ipt = kTok4 >> bs_log2;  // blocks per tile
 
     // ---- one round of independent loads: positions, queries, this split's selection ----
     const int a0 = split * items_per_split;
@@ -323,49 +322,54 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
 
     const int tlast = s_tlast;
     const int n_tiles = (n_blk + ipt - 1) / ipt;
-    // four threads per token row, each copying one 16-byte chunk of K and one of V codes;
-    // the first two also the row's K and V scales
-    constexpr int kRowsPerPass = kT / 4;
+    const uint32_t ring = sbase + SL.ring + warp * (D * kTile4);
+    int* s_tok = reinterpret_cast<int*>(smem + SL.tok) + warp * (D * kTok4);
+    // One tile into a slot of the warp's ring; returns whether some token of it is absent or
+    // not visible to every row (then the tokens' positions are in s_tok).
     auto load_tile = [&](int tile, int slot) {
-        const int q4 = tid & 3;
-        const uint32_t st = sbase + SL.stage + slot * kStage4;
-#pragma unroll
-        for (int u = 0; u < kTok4 / kRowsPerPass; ++u) {
-            const int row = (tid >> 2) + u * kRowsPerPass;
-            const int it = tile * ipt + (row >> bs_log2);
-            const int tin = row & (bs - 1);
-            long long off = -1;
-            int tp = INT_MAX;
-            if (it < n_blk) {
-                off = s_ioff[it];
-                const int ip = s_ipos[it];
-                if (off >= 0 && ip >= 0 && ip + tin > tlast) off = -1;  // past the group's last draft token
-                if (off >= 0) tp = ip < 0 ? -1 : ip + tin;
+        const uint32_t st = ring + slot * kTile4;
+        // lane = token row: its place in the cache, its scales
+        const int it = tile * ipt + (lane >> bs_log2), tin = lane & (bs - 1);
+        long long e = -1;
+        int tp = INT_MAX;
+        if (it < n_blk) {
+            e = s_ioff[it];
+            const int ip = s_ipos[it];
+            if (ip >= 0 && ip + tin > tlast) e = -1;       // past the group's last draft token
+            if (e >= 0) {
+                e += tin;
+                tp = ip < 0 ? -1 : ip + tin;
             }
-            const int n16 = off >= 0 ? 16 : 0, n8 = off >= 0 ? 8 : 0;
-            const long long e = off >= 0 ? off + tin : 0;
-            // token tt of a warp's 16: K in the order the MMA rows read it, V by token with
-            // the chunk's upper bit flipped every two tokens (both reads without conflicts)
-            const int grp16 = row >> 4, tt = row & 15;
-            const uint32_t kpos = grp16 * 1024 + ((tt & 3) + ((tt >> 3) << 2)) * 128 + ((tt >> 2) & 1) * 64 + q4 * 16;
-            const uint32_t vpos = kCodes + row * 64 + ((q4 ^ (tt & 2)) << 4);
-            cp_async16(st + kpos, k_codes + e * kCodeRow + q4 * 16, n16);
-            cp_async16(st + vpos, v_codes + e * kCodeRow + q4 * 16, n16);
-            if (q4 == 0) cp_async8(st + 2 * kCodes + row * 8, k_scales + e * kScaleRow, n8);
-            if (q4 == 1) cp_async8(st + 2 * kCodes + kScales + row * 8, v_scales + e * kScaleRow, n8);
-            if (q4 == 0) s_tok[slot * kTok4 + row] = tp;
         }
+        const long long es = e >= 0 ? e : 0;
+        cp_async8(st + 2 * kCodes + lane * 8, k_scales + es * kScaleRow, e >= 0 ? 8 : 0);
+        cp_async8(st + 2 * kCodes + kScales + lane * 8, v_scales + es * kScaleRow, e >= 0 ? 8 : 0);
+        // four lanes per row, a 16-byte chunk of K and of V codes each; the upper bit of V's
+        // chunk is flipped every two tokens, so that the reads below meet no bank twice
+        const int q4 = lane & 3;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int row = (lane >> 2) + 8 * u;
+            const long long er = __shfl_sync(0xffffffffu, e, row);
+            const long long src = (er >= 0 ? er : 0) * kCodeRow + q4 * 16;
+            const int n16 = er >= 0 ? 16 : 0;
+            cp_async16(st + row * 64 + q4 * 16, k_codes + src, n16);
+            cp_async16(st + kCodes + row * 64 + ((q4 ^ (row & 2)) << 4), v_codes + src, n16);
+        }
+        cp_commit();
+        const bool special = __any_sync(0xffffffffu, tp != -1);
+        if (special) s_tok[slot * kTok4 + lane] = tp;
+        return special;
     };
 
-    // every slot is filled at once; later tiles refill the slots of a finished round
-    int issued = 0;
-    for (; issued < n_stages && issued < n_tiles; ++issued) {
-        load_tile(issued, issued);
-        cp_commit();
+    unsigned special = 0;            // bit per slot
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+        const int t = warp + u * KW;
+        if (t < n_tiles) special |= (unsigned)load_tile(t, u) << u;
+        else cp_commit();
     }
 
-    const int wg = warp >> 2;        // compute group
-    const int wq = warp & 3;         // warp within the group: 16 tokens of the stage
     const int c4 = lane & 3, l4 = lane >> 2;
     int trow[NT][2];
     float rsc[NT][2];                // logit scale of the lane's accumulator columns
@@ -398,30 +402,29 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
-    const int tt_lo = (l4 >> 1) + ((l4 & 1) << 2);   // token (of 16) of MMA row l4; row l4 + 8 holds tt_lo + 8
+    // token (of 16) of MMA row r, in either half of a tile: r / 2 for even r, 4 + (r / 2 ^ 1) for
+    // odd r, + 8 for rows 8 and up.  Two neighbouring rows lie in different halves of 128 bytes
+    // (K's reads), the even rows are tokens 0 to 3 (V's reads)
+    const int tk = l4 & 1 ? 4 + ((l4 >> 1) ^ 1) : l4 >> 1;
+    const int tv0 = c4, tv1 = 4 + (c4 ^ 1);   // of rows 2 c4 and 2 c4 + 1
 
-    for (int r0 = 0; r0 < n_tiles; r0 += NWG) {
-        // tiles r0 .. r0 + NWG - 1 have landed (this thread's copies), then every thread's
-        const int done = min(n_tiles, r0 + NWG);
-        cp_wait_pending(issued - done);
-        __syncthreads();
-        const int tile = r0 + wg;
-        const int slot = tile % n_stages;
-        const uint32_t st = sbase + SL.stage + slot * kStage4;
-        const bool have = tile < n_tiles;
-        const int tp0 = have ? s_tok[slot * kTok4 + 16 * wq + tt_lo] : INT_MAX;
-        const int tp1 = have ? s_tok[slot * kTok4 + 16 * wq + tt_lo + 8] : INT_MAX;
-
-        if (__any_sync(0xffffffffu, tp0 != INT_MAX || tp1 != INT_MAX)) {  // skip a warp's empty tokens
-            // ---- S^T = K Q^T: rows l4 and l4 + 8, dims 32 c4 + 8 w .. + 7 per word ----
-            float sa[NT][4], sb[NT][4];
+    int slot = 0;
+    for (int t = warp; t < n_tiles; t += KW) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(D - 1));
+        __syncwarp();
+        const uint32_t st = ring + slot * kTile4;
+        const bool masked = special >> slot & 1u;
+        // ---- S^T = K Q^T: rows l4 and l4 + 8 of each half, dims 32 c4 + 8 w .. + 7 per word ----
+        float sc[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sa[nt][e] = sb[nt][e] = 0.f;
-            const uint4 k0 = lds128(st + wq * 1024 + l4 * 64 + c4 * 16);
-            const uint4 k1 = lds128(st + wq * 1024 + 512 + l4 * 64 + c4 * 16);
-            const uint32_t ksc = st + 2 * kCodes + (16 * wq + tt_lo) * 8 + 2 * c4;
+                for (int e = 0; e < 4; ++e) sc[h][nt][e] = 0.f;
+            const uint32_t kr = st + (16 * h + tk) * 64 + c4 * 16;
+            const uint4 k0 = lds128(kr), k1 = lds128(kr + 512);
+            const uint32_t ksc = st + 2 * kCodes + (16 * h + tk) * 8 + 2 * c4;
             const uint32_t s0 = unpack_e4m3x2(lds16(ksc)), s1 = unpack_e4m3x2(lds16(ksc + 64));
             const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
@@ -442,73 +445,96 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     if constexpr (kHoldQ) {
-                        mma16816_f16(sa[nt], ka, qb[w][nt][0], qb[w][nt][1]);
-                        mma16816_f16(sb[nt], kb, qb[w][nt][2], qb[w][nt][3]);
+                        mma16816_f16(sc[h][nt], ka, qb[w][nt][0], qb[w][nt][1]);
+                        mma16816_f16(sc[h][nt], kb, qb[w][nt][2], qb[w][nt][3]);
                     } else {
                         const uint4 v = lds128(sbase + swz_q(8 * nt + l4, 4 * c4 + w));
-                        mma16816_f16(sa[nt], ka, v.x, v.y);
-                        mma16816_f16(sb[nt], kb, v.z, v.w);
+                        mma16816_f16(sc[h][nt], ka, v.x, v.y);
+                        mma16816_f16(sc[h][nt], kb, v.z, v.w);
                     }
                 }
             }
-            uint32_t pb[NT][2];
+        }
+        // ---- softmax: element e of half h: token 16 h + tk (+8 for e >= 2), row 8nt + 2c4 + (e & 1) ----
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                // element e: token tt_lo (+8 for e >= 2), row 8nt + 2c4 + (e & 1)
-                float x[4];
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int tp = e < 2 ? tp0 : tp1;
-                    x[e] = tp <= trow[nt][e & 1] ? (sa[nt][e] + sb[nt][e]) * rsc[nt][e & 1] : -INFINITY;
-                }
-                float a[2];
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[h][nt][e] *= rsc[nt][e & 1];
+        if (masked) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int tp0 = s_tok[slot * kTok4 + 16 * h + tk], tp1 = s_tok[slot * kTok4 + 16 * h + tk + 8];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if ((e < 2 ? tp0 : tp1) > trow[nt][e & 1]) sc[h][nt][e] = -INFINITY;
+            }
+        }
+        float mx[NT][2];
+        bool grow = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = fmaxf(fmaxf(sc[0][nt][j], sc[0][nt][j + 2]), fmaxf(sc[1][nt][j], sc[1][nt][j + 2]));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                mx[nt][j] = x;
+                grow = grow || x > m[nt][j] + kGrow4;
+            }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float mx = fmaxf(x[j], x[j + 2]);
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float mn = fmaxf(m[nt][j], mx);
-                    const float mu = mn == -INFINITY ? 0.f : mn;
-                    a[j] = exp2f(m[nt][j] - mu);
-                    const float p0 = exp2f(x[j] - mu + kProbShift), p1 = exp2f(x[j + 2] - mu + kProbShift);
-                    x[j] = p0;
-                    x[j + 2] = p1;
-                    l[nt][j] = l[nt][j] * a[j] + (p0 + p1);
-                    m[nt][j] = mn;
-                }
+                    const bool g_ = mx[nt][j] > m[nt][j] + kGrow4;
+                    const float f = g_ ? exp2_approx(m[nt][j] - mx[nt][j]) : 1.0f;
+                    if (g_) m[nt][j] = mx[nt][j];
+                    l[nt][j] *= f;
 #pragma unroll
-                for (int mt = 0; mt < 8; ++mt) {
-                    o[mt][nt][0] *= a[0];
-                    o[mt][nt][1] *= a[1];
-                    o[mt][nt][2] *= a[0];
-                    o[mt][nt][3] *= a[1];
+                    for (int mt = 0; mt < 8; ++mt) {
+                        o[mt][nt][j] *= f;
+                        o[mt][nt][j + 2] *= f;
+                    }
                 }
-                pb[nt][0] = movm_t(pack_f16(x[0], x[1]));  // MMA rows 0-7 -> B operand (k = token, n = row)
-                pb[nt][1] = movm_t(pack_f16(x[2], x[3]));  // rows 8-15
+        }
+        uint32_t pb[2][NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float u0 = kProbShift - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]);
+            const float u1 = kProbShift - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float p0 = exp2_approx(sc[h][nt][0] + u0), p1 = exp2_approx(sc[h][nt][1] + u1);
+                const float p2 = exp2_approx(sc[h][nt][2] + u0), p3 = exp2_approx(sc[h][nt][3] + u1);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                pb[h][nt][0] = movm_t(pack_f16(p0, p1));  // MMA rows 0-7 -> B operand (k = token, n = row)
+                pb[h][nt][1] = movm_t(pack_f16(p2, p3));  // rows 8-15
             }
-            // ---- O^T += V^T P^T: tokens c4, c4 + 4 (k pair 0) and c4 + 8, c4 + 12 (k pair 1) ----
-            const int tv = 16 * wq + c4;
+        }
+        // ---- O^T += V^T P^T: token pairs (tv0, tv1) and (tv0 + 8, tv1 + 8) of each half ----
+        int bad = INT_MAX;           // first tail token whose group l4 is NaN
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
             uint2 vw[4];
             uint32_t vs[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int t = tv + 4 * u;
-                vw[u] = lds64(st + kCodes + t * 64 + (((l4 >> 1) ^ (t & 2)) << 4) + (l4 & 1) * 8);
-                vs[u] = lds8(st + 2 * kCodes + kScales + t * 8 + l4);
-            }
-            int bad = INT_MAX;       // first tail token whose group l4 is NaN
-            if (group_q > 1 && __any_sync(0xffffffffu, (tp0 >= 0 && tp0 != INT_MAX) || (tp1 >= 0 && tp1 != INT_MAX))) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int tp = s_tok[slot * kTok4 + tv + 4 * u];
+                const int tt = 16 * h + (u & 1 ? tv1 : tv0) + (u & 2 ? 8 : 0);
+                vw[u] = lds64(st + kCodes + tt * 64 + (((l4 >> 1) ^ (tt & 2)) << 4) + (l4 & 1) * 8);
+                vs[u] = lds8(st + 2 * kCodes + kScales + tt * 8 + l4);
+                if (masked && group_q > 1) {
+                    const int tp = s_tok[slot * kTok4 + tt];
                     if (tp >= 0 && tp != INT_MAX && (vs[u] & 0x7Fu) == 0x7Fu) {
                         bad = min(bad, tp);
                         vs[u] = 0;
                     }
                 }
-                bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 1));
-                bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 2));
             }
             const uint32_t g0 = unpack_e4m3x2(vs[0] | (vs[1] << 8)), g1 = unpack_e4m3x2(vs[2] | (vs[3] << 8));
 #pragma unroll
@@ -529,10 +555,14 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
                     const uint32_t va[4] = {mul_f16x2(e0[i], g0), mul_f16x2(d0[i], g0), mul_f16x2(e1[i], g1),
                                             mul_f16x2(d1[i], g1)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[mt][nt], va, pb[nt][0], pb[nt][1]);
+                    for (int nt = 0; nt < NT; ++nt) mma16816_f16(o[mt][nt], va, pb[h][nt][0], pb[h][nt][1]);
                 }
             }
-            if (__any_sync(0xffffffffu, bad != INT_MAX)) {
+        }
+        if (masked && group_q > 1) {
+            bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 1));
+            bad = min(bad, __shfl_xor_sync(0xffffffffu, bad, 2));
+            if (bad != INT_MAX) {
 #pragma unroll
                 for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
@@ -542,17 +572,16 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
                             if (trow[nt][e & 1] >= bad) o[mt][nt][e] = __int_as_float(0x7FC00000);
             }
         }
-        __syncthreads();  // every warp is done with this round's slots
-        for (int u = 0; u < NWG && issued < n_tiles; ++u) {
-            load_tile(issued, issued % n_stages);
-            cp_commit();
-            ++issued;
-        }
+        __syncwarp();                // every lane is done with the slot
+        special &= ~(1u << slot);
+        if (t + D * KW < n_tiles) special |= (unsigned)load_tile(t + D * KW, slot) << slot;
+        else cp_commit();
+        slot = slot + 1 == D ? 0 : slot + 1;
     }
-    cp_wait_pending(0);
+    asm volatile("cp.async.wait_group 0;\n" ::);
     __syncthreads();
 
-    // ---- merge the warps: (m, l) per row, O^T into shared memory (stage area) ----
+    // ---- merge the warps: (m, l) per row, O^T into shared memory (ring area) ----
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -561,9 +590,9 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
             l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
             l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
         }
-    float* s_o = reinterpret_cast<float*>(smem + SL.stage);  // [kW][RP][128]
-    float* s_m = s_o + kW * RP * kHeadDim;                // [kW][RP]
-    float* s_l = s_m + kW * RP;                           // [kW][RP]
+    float* s_o = reinterpret_cast<float*>(smem + SL.ring);  // [KW][RP][128]
+    float* s_m = s_o + KW * RP * kHeadDim;                // [KW][RP]
+    float* s_l = s_m + KW * RP;                           // [KW][RP]
     if (l4 == 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -587,46 +616,49 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         }
     __syncthreads();
 
-    constexpr int TPR = kT / RP;          // threads per row
-    constexpr int DPT = kHeadDim / TPR;   // dims per thread: 4 .. 32
-    const int row = tid / TPR, d0 = (tid % TPR) * DPT;
+    constexpr int TPR = kT / RP < 32 ? kT / RP : 32;   // threads per row; with more, the rest look on
+    constexpr int DPT = kHeadDim / TPR;                // dims per thread: 4 .. 32
+    const bool mine = tid < RP * TPR;
+    const int row = mine ? tid / TPR : 0, d0 = (tid % TPR) * DPT;
     float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) M = fmaxf(M, s_m[w * RP + row]);
+    for (int w = 0; w < KW; ++w) M = fmaxf(M, s_m[w * RP + row]);
     const float Mu = M == -INFINITY ? 0.f : M;
     float L = 0.f, acc[DPT];
 #pragma unroll
     for (int e = 0; e < DPT; ++e) acc[e] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
+    for (int w = 0; w < KW; ++w) {
         const float f = exp2f(s_m[w * RP + row] - Mu);
         L += s_l[w * RP + row] * f;
 #pragma unroll
         for (int e = 0; e < DPT; ++e) acc[e] += s_o[(w * RP + row) * kHeadDim + d0 + e] * f;
     }
-    const bool live_row = row < R;
+    const bool live_row = mine && row < R;
 
     if (n_split > 1) {
         // the n_split CTAs of this (group, KV head) form one cluster: partials meet in
         // the first CTA's shared memory; every thread of every CTA reaches both barriers
         namespace cg = cooperative_groups;
         cg::cluster_group cl = cg::this_cluster();
-        cl.sync();  // every CTA has finished its warp merge: stage areas are free
-        float* lead = cl.map_shared_rank(reinterpret_cast<float*>(smem + SL.stage), 0);
+        cl.sync();  // every CTA has finished its warp merge: ring areas are free
+        float* lead = cl.map_shared_rank(reinterpret_cast<float*>(smem + SL.ring), 0);
         float* po = lead;                                       // [n_split][RP][128]
         float* pm = lead + (size_t)n_split * RP * kHeadDim;     // [n_split][RP]
         float* pl = pm + n_split * RP;                          // [n_split][RP]
-        if ((tid % TPR) == 0) {
-            pm[split * RP + row] = M;
-            pl[split * RP + row] = L;
-        }
+        if (live_row) {
+            if (d0 == 0) {
+                pm[split * RP + row] = M;
+                pl[split * RP + row] = L;
+            }
 #pragma unroll
-        for (int e = 0; e < DPT; e += 4)
-            *reinterpret_cast<float4*>(po + (split * RP + row) * kHeadDim + d0 + e) =
-                make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+            for (int e = 0; e < DPT; e += 4)
+                *reinterpret_cast<float4*>(po + (split * RP + row) * kHeadDim + d0 + e) =
+                    make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
+        }
         cl.sync();
         if (split != 0 || !live_row) return;
-        const float* lpo = reinterpret_cast<const float*>(smem + SL.stage);
+        const float* lpo = reinterpret_cast<const float*>(smem + SL.ring);
         const float* lpm = lpo + (size_t)n_split * RP * kHeadDim;
         const float* lpl = lpm + n_split * RP;
         M = -INFINITY;
@@ -665,28 +697,44 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
 namespace {
 
 int nt_for(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
-// compute groups: two for up to 16 rows; one for 32 (its accumulators fill the registers)
-int nwg_for(int nt) { return nt <= 2 ? 2 : 1; }
 
-const void* kernel4(int nt)
+// One kernel per row tile count and call shape.  Few pairs: one CTA per SM, as many warps as
+// its registers allow; many pairs: smaller CTAs, several per SM.
+struct Shape {
+    const void* fn;
+    int warps, depth;
+};
+Shape shape4(int nt, bool many)
 {
-    return nt == 1 ? (const void*)k_sparse_attn_kv4<1, 2>
-                   : nt == 2 ? (const void*)k_sparse_attn_kv4<2, 2> : (const void*)k_sparse_attn_kv4<4, 1>;
+    if (nt == 1)
+        return many ? Shape{(const void*)k_sparse_attn_kv4<1, 8, 2>, 8, 2} : Shape{(const void*)k_sparse_attn_kv4<1, 16, 2>, 16, 2};
+    if (nt == 2) return Shape{(const void*)k_sparse_attn_kv4<2, 8, 2>, 8, 2};
+    return Shape{(const void*)k_sparse_attn_kv4<4, 8, 2>, 8, 2};
 }
 
-bool configure4(int dev, int nt)
+constexpr int kMaxArea = 160 * 1024;   // of the rings and merge buffers
+
+bool configure4(int dev, int nt, bool many)
 {
-    static std::atomic<bool> done[64][3];
-    const int ni = nt == 1 ? 0 : nt == 2 ? 1 : 2;
+    static std::atomic<bool> done[64][6];
+    const int ni = (nt == 1 ? 0 : nt == 2 ? 1 : 2) + (many ? 3 : 0);
     if (dev < 0 || dev >= 64) return false;
     if (done[dev][ni].load()) return true;
-    const void* fn = kernel4(nt);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, layout4(8 * nt, kMaxStages4).total) !=
-            cudaSuccess ||
-        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    const Shape s = shape4(nt, many);
+    if (cudaFuncSetAttribute(s.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             layout4(8 * nt, s.warps, s.depth, kMaxArea).total) != cudaSuccess ||
+        cudaFuncSetAttribute(s.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return false;
     done[dev][ni].store(true);
     return true;
+}
+
+int area4(int rp, const Shape& s, int ns)
+{
+    // the rings, then the warps' and the cluster's partials
+    const int part = rp * (kHeadDim + 2) * 4, parts = ns > s.warps ? ns : s.warps;
+    const int rings = s.warps * s.depth * kTile4;
+    return rings > parts * part ? rings : parts * part;
 }
 
 }  // namespace
@@ -694,26 +742,22 @@ bool configure4(int dev, int nt)
 void plan_kv4(const qsa_dims& d, int64_t n_groups, int group_q, qsa_attn_plan_info* p)
 {
     const int rows = d.n_q_heads / d.n_kv_heads * group_q;
-    const int nt = nt_for(rows), nwg = nwg_for(nt), rp = 8 * nt;
+    const int nt = nt_for(rows), rp = 8 * nt;
     const int64_t pairs = n_groups * d.n_kv_heads;
+    const bool many = pairs >= 148;
+    const Shape s = shape4(nt, many);
     const int ipt = kTok4 / d.block_size;
     const int tiles_max = (kItems4 + ipt - 1) / ipt;
-    int ns = pairs >= 148 ? 1 : (int)(148 / pairs > kMaxSplits4 ? kMaxSplits4 : 148 / pairs);
+    int ns = many ? 1 : (int)(148 / pairs > kMaxSplits4 ? kMaxSplits4 : 148 / pairs);
     if (ns > tiles_max) ns = tiles_max;
     const int part = rp * (kHeadDim + 2) * 4;      // one split's partial in the merge buffer
-    if (ns * part > kMaxStages4 * kStage4) ns = kMaxStages4 * kStage4 / part;
+    if (ns * part > kMaxArea) ns = kMaxArea / part;
     const int tiles = (tiles_max + ns - 1) / ns;
     ns = (tiles_max + tiles - 1) / tiles;          // no split without a tile
-    // few pairs: everything in flight at once; many: a short ring, several CTAs per SM
-    int st = ns == 1 && pairs >= 148 ? 4 : tiles < kMaxStages4 ? tiles : kMaxStages4;
-    if (st < 2 * nwg) st = 2 * nwg;
-    // the warps' (and the cluster's) merge buffers live in the stage area
-    const int merge = (ns > 4 * nwg ? ns : 4 * nwg) * part;
-    while (st * kStage4 < merge) ++st;
     p->n_split = ns;
-    p->n_stages = st;
-    p->threads = 128 * nwg;
-    p->smem_bytes = layout4(rp, st).total;
+    p->n_stages = s.warps * s.depth;
+    p->threads = 32 * s.warps;
+    p->smem_bytes = layout4(rp, s.warps, s.depth, area4(rp, s, ns)).total;
     p->ctas = pairs * ns;
     p->cluster_merge = ns > 1;
     p->rows = rows;
@@ -724,18 +768,19 @@ cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, co
                                    int64_t n_groups, int group_q, void* out, unsigned* status, cudaStream_t st)
 {
     if (n_groups <= 0) return cudaSuccess;
-    const int rows = d.n_q_heads / d.n_kv_heads * group_q;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const int nt = nt_for(rows);
-    if (!configure4(dev, nt)) return cudaErrorInvalidValue;
-    int bs_log2 = 0;
-    while ((1 << bs_log2) < d.block_size) ++bs_log2;
     qsa_attn_plan_info p;
     plan_kv4(d, n_groups, group_q, &p);
-    const int n_split = p.n_split;
-    const int tiles_max = (kItems4 + kTok4 / d.block_size - 1) / (kTok4 / d.block_size);
-    const int items = (tiles_max + n_split - 1) / n_split * (kTok4 / d.block_size);   // of one split, in whole stages
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const int nt = nt_for(p.rows);
+    const bool many = n_groups * d.n_kv_heads >= 148;
+    if (!configure4(dev, nt, many)) return cudaErrorInvalidValue;
+    int bs_log2 = 0;
+    while ((1 << bs_log2) < d.block_size) ++bs_log2;
+    const int n_split = p.n_split, ipt = kTok4 >> bs_log2;
+    const int tiles_max = (kItems4 + ipt - 1) / ipt;
+    const int items = (tiles_max + n_split - 1) / n_split * ipt;   // of one split, in whole tiles
+    const int area = area4(8 * nt, shape4(nt, many), n_split);
     const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / sqrtf((float)d.head_dim);
 
     cudaLaunchConfig_t cfg = {};
@@ -757,9 +802,10 @@ cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, co
             (const uint8_t*)c.v_codes, (const uint8_t*)c.v_scales, q_seq, q_pos, sel_idx, sel_cnt, c.page_table,
             (int)c.page_tokens, c.page_table ? d.kv_capacity / c.page_tokens : (int64_t)0, c.n_pages, (int)d.batch,
             (int)d.n_q_heads, (int)d.n_kv_heads, d.kv_capacity, bs_log2, (int)d.top_k, group_q,
-            scale * 1.4426950408889634f, items, n_split, (int)p.n_stages, (__nv_bfloat16*)out, status);
+            scale * 1.4426950408889634f, items, n_split, area, (__nv_bfloat16*)out, status);
     };
-    return nt == 1 ? go(k_sparse_attn_kv4<1, 2>) : nt == 2 ? go(k_sparse_attn_kv4<2, 2>) : go(k_sparse_attn_kv4<4, 1>);
+    if (nt == 1) return many ? go(k_sparse_attn_kv4<1, 8, 2>) : go(k_sparse_attn_kv4<1, 16, 2>);
+    return nt == 2 ? go(k_sparse_attn_kv4<2, 8, 2>) : go(k_sparse_attn_kv4<4, 8, 2>);
 }
 
 }  // namespace qsa

@@ -191,17 +191,17 @@ def test_kv4_plans_fit_the_hardware(qsa):
         d = qsa.make_dims(1, rows, 1, 65536, block_size=bs)
         info = qsa.qsa_attn_plan_info()
         assert qsa.load().qsa_attn_kv4_plan(ctypes.byref(d), pairs, 1, ctypes.byref(info)) == qsa.QSA_OK
-        per_stage = 64 // bs
-        tiles = math.ceil(514 / per_stage)
+        per_tile = 32 // bs
+        tiles = math.ceil(514 / per_tile)
         assert 1 <= info.n_split <= 16 and info.rows == rows and info.ctas == pairs * info.n_split
         assert info.n_split == 1 or info.ctas <= 148
-        assert 1 <= info.n_stages <= 16
         own = math.ceil(tiles / info.n_split)
         assert (info.n_split - 1) * own < tiles            # the last split has a tile
-        assert own * per_stage <= 592                      # items of a split fit their list
+        assert own * per_tile <= 576                       # items of a split fit their list
         warps = info.threads // 32
-        assert max(info.n_split, warps) * rp * 130 * 4 <= info.n_stages * 9216
-        assert info.smem_bytes >= rp * 256 + info.n_stages * (9216 + 256) + 592 * 12 + 256
+        assert info.n_stages % warps == 0 and 1 <= info.n_stages // warps
+        area = max(info.n_stages * 4608, max(info.n_split, warps) * rp * 130 * 4)   # rings, then partials
+        assert info.smem_bytes >= rp * 256 + area + info.n_stages * 128 + 576 * 12 + 256
         assert info.smem_bytes + 1024 <= 227 * 1024
 
 
