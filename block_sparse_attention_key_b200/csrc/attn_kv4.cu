@@ -15,8 +15,8 @@
 //
 // Work unit and splits: one CTA per (split, KV head, draft group), its rows the group's
 // query heads of that KV head (<= 32), tokens on the M side of mma.sync m16n8k16.  The
-// splits of a (group, KV head) form one thread-block cluster and merge in its first CTA's
-// shared memory, so a call needs no scratch.  What differs from a bf16 gather is that
+// splits of a (group, KV head) form one thread-block cluster and read one another's partials
+// through shared memory, each finishing a share of the rows, so a call needs no scratch.  What differs from a bf16 gather is that
 // unpacking, not the copies, is the work (about 500 instructions per warp and 32 tokens,
 // 2.3 KB of each K and V), so operands never pass through shared memory unpacked and
 // warps do not wait for one another: each takes 32 tokens at a time through a ring of its
@@ -226,13 +226,12 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     const int cnt_raw = tid == 0 ? __ldg(sel_cnt + grp) : 0;
     if (warp == 0) {
         // lane r < RP: row r = (draft query j = r / G, head r % G); its position, or -2
-        const int s0 = q_seq[qi0], t0 = q_pos[qi0];
+        const int64_t qi = qi0 + (lane < R ? lane / G : 0);
+        const int s0 = __ldg(q_seq + qi0), t0 = __ldg(q_pos + qi0), sj = __ldg(q_seq + qi), tj = __ldg(q_pos + qi);
         const bool ok0 = s0 >= 0 && s0 < batch && t0 >= 0 && (int64_t)t0 < kv_capacity;
         const int nc0 = ok0 ? (int)(((int64_t)t0 + 1) >> bs_log2) : 0;
         int t = -2;
         if (lane < R && ok0) {
-            const int j = lane / G;
-            const int sj = q_seq[qi0 + j], tj = q_pos[qi0 + j];
             // a draft query follows the selection's query within the two tail blocks
             const bool ok = sj == s0 && tj >= t0 && (int64_t)tj <= (int64_t)bs * nc0 + 2 * bs - 1 &&
                             (int64_t)tj < kv_capacity;
@@ -250,8 +249,9 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
                 set_status(status, (s0 < 0 || s0 >= batch) ? QSA_DEV_BAD_SEQ : QSA_DEV_BAD_POS);
         }
     }
-    // query rows in fp16, 16 threads per row: the row's largest magnitude goes to [2^14, 2^15)
-    for (int k = tid; k < RP * 16; k += kT) {
+    // query rows in fp16, 16 threads per row: the row's largest magnitude goes to [2^14, 2^15);
+    // by the last warps, beside the first one's loads
+    for (int k = kT - 1 - tid; k < RP * 16; k += kT) {
         const int row = k >> 4, ch = k & 15;
         uint4 v = make_uint4(0, 0, 0, 0);
         if (row < R) v = __ldg(q + ((qi0 + row / G) * n_q_heads + (int64_t)g * G + row % G) * 16 + ch);
@@ -590,9 +590,12 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
             l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 8);
             l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], 16);
         }
-    float* s_o = reinterpret_cast<float*>(smem + SL.ring);  // [KW][RP][128]
-    float* s_m = s_o + KW * RP * kHeadDim;                // [KW][RP]
-    float* s_l = s_m + KW * RP;                           // [KW][RP]
+    // O in 16-byte pieces, piece c of row r at place c ^ (r / 2 & 3): eight lanes that store together
+    // hold rows 2 c4 + j and pieces 4 l4 + n of two l4, which are then in different banks
+    float4* s_o = reinterpret_cast<float4*>(smem + SL.ring);  // [KW][RP][32]
+    float* s_m = reinterpret_cast<float*>(s_o + KW * RP * 32);  // [KW][RP]
+    float* s_l = s_m + KW * RP;                                 // [KW][RP]
+    auto piece = [](int row, int c) { return row * 32 + (c ^ (row >> 1 & 3)); };
     if (l4 == 0) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -608,88 +611,91 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         for (int j = 0; j < 2; ++j) {
             // 16 consecutive dims of one row per lane
             const int row = 8 * nt + 2 * c4 + j;
-            float* po = s_o + (warp * RP + row) * kHeadDim + 16 * l4;
 #pragma unroll
             for (int mt = 0; mt < 8; mt += 2)
-                *reinterpret_cast<float4*>(po + 2 * mt) =
+                s_o[warp * RP * 32 + piece(row, 4 * l4 + mt / 2)] =
                     make_float4(o[mt][nt][j], o[mt][nt][j + 2], o[mt + 1][nt][j], o[mt + 1][nt][j + 2]);
         }
     __syncthreads();
 
-    constexpr int TPR = kT / RP < 32 ? kT / RP : 32;   // threads per row; with more, the rest look on
-    constexpr int DPT = kHeadDim / TPR;                // dims per thread: 4 .. 32
-    const bool mine = tid < RP * TPR;
-    const int row = mine ? tid / TPR : 0, d0 = (tid % TPR) * DPT;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) M = fmaxf(M, s_m[w * RP + row]);
-    const float Mu = M == -INFINITY ? 0.f : M;
-    float L = 0.f, acc[DPT];
-#pragma unroll
-    for (int e = 0; e < DPT; ++e) acc[e] = 0.f;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
-        const float f = exp2f(s_m[w * RP + row] - Mu);
-        L += s_l[w * RP + row] * f;
-#pragma unroll
-        for (int e = 0; e < DPT; ++e) acc[e] += s_o[(w * RP + row) * kHeadDim + d0 + e] * f;
+    // ---- merge the warps: a thread per row and 4 dims ----
+    namespace cg = cooperative_groups;
+    constexpr int kPieces = RP * 32;
+    float4* s_mo = s_o;                                       // [RP][32] merged, in the place of warp 0's
+    float* s_mm = reinterpret_cast<float*>(smem + SL.tok);    // [RP], [RP] merged (the positions are no longer needed)
+    float* s_ml = s_mm + RP;
+    for (int k = tid; k < kPieces; k += kT) {
+        const int row = k >> 5, c = k & 31;
+        float M = -INFINITY;
+#pragma unroll 4
+        for (int w = 0; w < KW; ++w) M = fmaxf(M, s_m[w * RP + row]);
+        const float Mu = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int w = 0; w < KW; ++w) {
+            const float f = exp2_approx(s_m[w * RP + row] - Mu);
+            const float4 v = s_o[w * kPieces + piece(row, c)];
+            L += s_l[w * RP + row] * f;
+            acc.x += v.x * f;
+            acc.y += v.y * f;
+            acc.z += v.z * f;
+            acc.w += v.w * f;
+        }
+        s_mo[piece(row, c)] = acc;       // read by this thread alone so far
+        if (c == 0) {
+            s_mm[row] = M;
+            s_ml[row] = L;
+        }
     }
-    const bool live_row = mine && row < R;
 
-    if (n_split > 1) {
-        // the n_split CTAs of this (group, KV head) form one cluster: partials meet in
-        // the first CTA's shared memory; every thread of every CTA reaches both barriers
-        namespace cg = cooperative_groups;
-        cg::cluster_group cl = cg::this_cluster();
-        cl.sync();  // every CTA has finished its warp merge: ring areas are free
-        float* lead = cl.map_shared_rank(reinterpret_cast<float*>(smem + SL.ring), 0);
-        float* po = lead;                                       // [n_split][RP][128]
-        float* pm = lead + (size_t)n_split * RP * kHeadDim;     // [n_split][RP]
-        float* pl = pm + n_split * RP;                          // [n_split][RP]
-        if (live_row) {
-            if (d0 == 0) {
-                pm[split * RP + row] = M;
-                pl[split * RP + row] = L;
-            }
-#pragma unroll
-            for (int e = 0; e < DPT; e += 4)
-                *reinterpret_cast<float4*>(po + (split * RP + row) * kHeadDim + d0 + e) =
-                    make_float4(acc[e], acc[e + 1], acc[e + 2], acc[e + 3]);
-        }
-        cl.sync();
-        if (split != 0 || !live_row) return;
-        const float* lpo = reinterpret_cast<const float*>(smem + SL.ring);
-        const float* lpm = lpo + (size_t)n_split * RP * kHeadDim;
-        const float* lpl = lpm + n_split * RP;
-        M = -INFINITY;
-        for (int sp = 0; sp < n_split; ++sp) M = fmaxf(M, lpm[sp * RP + row]);
-        const float mu = M == -INFINITY ? 0.f : M;
-        L = 0.f;
-#pragma unroll
-        for (int e = 0; e < DPT; ++e) acc[e] = 0.f;
-        for (int sp = 0; sp < n_split; ++sp) {
-            const float f = exp2f(lpm[sp * RP + row] - mu);
-            L += lpl[sp * RP + row] * f;
-#pragma unroll
-            for (int e = 0; e < DPT; e += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(lpo + (sp * RP + row) * kHeadDim + d0 + e);
-                acc[e] += v.x * f;
-                acc[e + 1] += v.y * f;
-                acc[e + 2] += v.z * f;
-                acc[e + 3] += v.w * f;
-            }
-        }
-    }
-    if (!live_row) return;
-    __nv_bfloat16* orow = out + ((qi0 + row / G) * n_q_heads + (int64_t)g * G + row % G) * kHeadDim + d0;
-    const float inv = L == 0.f ? 0.f : 1.f / L;   // a row that attends nothing is 0; a NaN sum stays NaN
-#pragma unroll
-    for (int e = 0; e < DPT; e += 4) {
+    // ---- merge the splits: each CTA of the cluster finishes its share of the pieces ----
+    auto store = [&](int row, int c, float4 a, float L) {
+        if (row >= R) return;
+        const float inv = L == 0.f ? 0.f : 1.f / L;   // a row that attends nothing is 0; a NaN sum stays NaN
         uint2 v;
-        v.x = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-        v.y = pack_bf16(acc[e + 2] * inv, acc[e + 3] * inv);
-        *reinterpret_cast<uint2*>(orow + e) = v;
+        v.x = pack_bf16(a.x * inv, a.y * inv);
+        v.y = pack_bf16(a.z * inv, a.w * inv);
+        *reinterpret_cast<uint2*>(out + ((qi0 + row / G) * n_q_heads + (int64_t)g * G + row % G) * kHeadDim + 4 * c) = v;
+    };
+    if (n_split == 1) {
+        __syncthreads();
+        for (int k = tid; k < kPieces; k += kT) store(k >> 5, k & 31, s_mo[piece(k >> 5, k & 31)], s_ml[k >> 5]);
+        return;
     }
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    // `width` lanes per piece, one per split, so that a share takes one round trip to the others
+    const int width = n_split <= 2 ? 2 : n_split <= 4 ? 4 : n_split <= 8 ? 8 : 16;
+    const int sp = tid & (width - 1);
+    for (int k0 = 0; k0 < kPieces; k0 += kT / width * n_split) {
+        const int k = k0 + tid / width * n_split + split;
+        const int row = k >> 5, c = k & 31;
+        float M = -INFINITY, L = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (sp < n_split && k < kPieces) {
+            M = *cl.map_shared_rank(s_mm + row, sp);
+            L = *cl.map_shared_rank(s_ml + row, sp);
+            acc = *cl.map_shared_rank(s_mo + piece(row, c), sp);
+        }
+        float Mg = M;
+        for (int o = width >> 1; o > 0; o >>= 1) Mg = fmaxf(Mg, __shfl_xor_sync(0xffffffffu, Mg, o));
+        const float f = exp2_approx(M - (Mg == -INFINITY ? 0.f : Mg));
+        L *= f;
+        acc.x *= f;
+        acc.y *= f;
+        acc.z *= f;
+        acc.w *= f;
+        for (int o = width >> 1; o > 0; o >>= 1) {
+            L += __shfl_xor_sync(0xffffffffu, L, o);
+            acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+            acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+            acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+            acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+        }
+        if (sp == 0 && k < kPieces) store(row, c, acc, L);
+    }
+    cl.sync();   // nobody's shared memory goes before all have read it
 }
 
 // ---------------------------------------------------------------- host side
@@ -729,12 +735,11 @@ bool configure4(int dev, int nt, bool many)
     return true;
 }
 
-int area4(int rp, const Shape& s, int ns)
+int area4(int rp, const Shape& s)
 {
-    // the rings, then the warps' and the cluster's partials
-    const int part = rp * (kHeadDim + 2) * 4, parts = ns > s.warps ? ns : s.warps;
-    const int rings = s.warps * s.depth * kTile4;
-    return rings > parts * part ? rings : parts * part;
+    // the rings, then the warps' partials
+    const int parts = s.warps * rp * (kHeadDim + 2) * 4, rings = s.warps * s.depth * kTile4;
+    return rings > parts ? rings : parts;
 }
 
 }  // namespace
@@ -750,14 +755,12 @@ void plan_kv4(const qsa_dims& d, int64_t n_groups, int group_q, qsa_attn_plan_in
     const int tiles_max = (kItems4 + ipt - 1) / ipt;
     int ns = many ? 1 : (int)(148 / pairs > kMaxSplits4 ? kMaxSplits4 : 148 / pairs);
     if (ns > tiles_max) ns = tiles_max;
-    const int part = rp * (kHeadDim + 2) * 4;      // one split's partial in the merge buffer
-    if (ns * part > kMaxArea) ns = kMaxArea / part;
     const int tiles = (tiles_max + ns - 1) / ns;
     ns = (tiles_max + tiles - 1) / tiles;          // no split without a tile
     p->n_split = ns;
     p->n_stages = s.warps * s.depth;
     p->threads = 32 * s.warps;
-    p->smem_bytes = layout4(rp, s.warps, s.depth, area4(rp, s, ns)).total;
+    p->smem_bytes = layout4(rp, s.warps, s.depth, area4(rp, s)).total;
     p->ctas = pairs * ns;
     p->cluster_merge = ns > 1;
     p->rows = rows;
@@ -780,7 +783,7 @@ cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, co
     const int n_split = p.n_split, ipt = kTok4 >> bs_log2;
     const int tiles_max = (kItems4 + ipt - 1) / ipt;
     const int items = (tiles_max + n_split - 1) / n_split * ipt;   // of one split, in whole tiles
-    const int area = area4(8 * nt, shape4(nt, many), n_split);
+    const int area = area4(8 * nt, shape4(nt, many));
     const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / sqrtf((float)d.head_dim);
 
     cudaLaunchConfig_t cfg = {};

@@ -200,7 +200,7 @@ def test_kv4_plans_fit_the_hardware(qsa):
         assert own * per_tile <= 576                       # items of a split fit their list
         warps = info.threads // 32
         assert info.n_stages % warps == 0 and 1 <= info.n_stages // warps
-        area = max(info.n_stages * 4608, max(info.n_split, warps) * rp * 130 * 4)   # rings, then partials
+        area = max(info.n_stages * 4608, warps * rp * 130 * 4)   # rings, then partials
         assert info.smem_bytes >= rp * 256 + area + info.n_stages * 128 + 576 * 12 + 256
         assert info.smem_bytes + 1024 <= 227 * 1024
 
