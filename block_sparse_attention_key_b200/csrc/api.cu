@@ -510,7 +510,7 @@ int qsa_kv4_append(const qsa_dims* dims, const qsa_kv4_cache* cache, const void*
     if (n_tok == 0) return QSA_OK;
     if (!kv4_aligned(cache) || !aligned16(k) || !aligned16(v) || !aligned16(cu_len) || !aligned16(len_before))
         return QSA_ERR_INVALID_ARG;
-    if ((int64_t)n_tok * dims->n_kv_heads > (1ll << 33)) return QSA_ERR_UNSUPPORTED;  // 16 rows of threads per CTA
+    if ((int64_t)n_tok * dims->n_kv_heads > (1ll << 30)) return QSA_ERR_UNSUPPORTED;  // rows are counted in 32 bits
     return cuda_status(launch_kv4_append(*dims, *cache, k, k_ld, v, v_ld, cu_len, len_before, n_tok,
                                          (unsigned*)workspace, (cudaStream_t)stream));
 }
@@ -586,6 +586,10 @@ int qsa_pages_update(const qsa_dims* dims, const qsa_page_pools* pools, int32_t*
     int rc = check_dims(dims);
     if (rc != QSA_OK) return rc;
     if (n_free < 0 || n_fork < 0) return QSA_ERR_INVALID_ARG;
+    // entries of the named rows are counted in 32 bits
+    if (pools && pools->page_tokens > 0 &&
+        (int64_t)(n_free > n_fork ? n_free : n_fork) * (dims->kv_capacity / pools->page_tokens) > INT32_MAX)
+        return QSA_ERR_UNSUPPORTED;
     if ((n_free > 0 && !aligned16(free_seq)) || (n_fork > 0 && (!aligned16(fork_src) || !aligned16(fork_dst))) ||
         !aligned16(len_before) || !aligned16(len_after))
         return QSA_ERR_INVALID_ARG;

@@ -1,10 +1,15 @@
 // Appending K and V rows to a cache held in 4 bits (blocks of 16 values: e2m1 codes and
 // one e4m3 scale).  For each 16 values x of a row of 128:
 //     s = e4m3( max|x| / 6 ) kept in [2^-9, 448],   c = e2m1( x / s ),
-// both rounded to nearest even; 6 is the largest e2m1 value.  The quotients are fp32
-// divisions: x has 8 significant bits and s 4, so x / s never comes near a border of two
-// codes without lying on it, and a rounded quotient decides as the exact one does.  A
-// block with a value that is not finite gets the scale NaN and codes 0.
+// both rounded to nearest even; 6 is the largest e2m1 value.  A block with a value that is
+// not finite gets the scale NaN and codes 0.
+//
+// x / s without a division per value: r = 1 / s rounded, y = x r, which is off by at most
+// 2^-23 of x / s.  A code changes at borders t of 1 to 3 significant bits.  x has 8
+// significant bits and t s at most 7 + 2 (4 bits of s times an odd part of t below 8), so
+// x / s is either a border exactly or at least 2^-9 of it away.  y with its mantissa
+// rounded to 11 bits is therefore on the side of the border that x / s is on, and is the
+// border where x / s is: the conversion then breaks the tie to even as for the quotient.
 //
 // Bytes only: 256 read and 72 written per row.  One thread per block of 16 (two 16-byte
 // loads, one 8-byte store of codes, 8 threads fill a row's 8 scale bytes), rows in the
@@ -51,12 +56,11 @@ k_kv4_append(const __nv_bfloat16* __restrict__ k, int64_t k_ld, const __nv_bfloa
                 set_status(status, QSA_DEV_BAD_LEN);
         }
     // row = (token, K or V, head); a warp holds four of them
-    const int64_t row = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) >> 3;
+    const uint32_t row = blockIdx.x * (kAppendThreads / 8) + (threadIdx.x >> 3);
     const int blk = threadIdx.x & 7;
-    const int per_tok = 2 * n_kv_heads;
-    const int64_t tok64 = row / per_tok;
-    const int in_tok = (int)(row - tok64 * per_tok);
-    const int tok = tok64 < n_tok ? (int)tok64 : -1;
+    const uint32_t per_tok = 2 * n_kv_heads, tok32 = row / per_tok;
+    const int in_tok = (int)(row - tok32 * per_tok);
+    const int tok = tok32 < (uint32_t)n_tok ? (int)tok32 : -1;
     int seq = -1, found = -1;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -104,8 +108,10 @@ k_kv4_append(const __nv_bfloat16* __restrict__ k, int64_t k_ld, const __nv_bfloa
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(s16) : "h"(s8));
     float s;
     asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}\n" : "=f"(s) : "r"(s16));
+    const float r = __frcp_rn(s);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = __fdiv_rn(x[e], s);
+    for (int e = 0; e < 16; ++e)   // (an infinite product stays infinite and saturates)
+        x[e] = __uint_as_float((__float_as_uint(x[e] * r) + 0x1000u) & 0xFFFFE000u);
     uint2 codes = make_uint2(pack_e2m1x8(x), pack_e2m1x8(x + 8));
     if (!finite) {
         codes = make_uint2(0u, 0u);

@@ -9,8 +9,8 @@
 //
 // Every decision is a function of the state alone (free pages are taken lowest first, in
 // the order of (sequence, place)), so results do not depend on timing.  The bookkeeping is
-// a few thousand integers with many dependent steps: one CTA of 1,024 threads, phases
-// separated by barriers, one round trip to memory per phase.  The page contents are moved
+// a few thousand integers with about ten dependent round trips to memory: one CTA of 1,024
+// threads, phases separated by barriers, the loads of a phase all under way at once.  The page contents are moved
 // by a second kernel, launched as a programmatic dependent, that reads the list the first
 // one left: 16 KiB per CTA step, every pool in one launch.
 
@@ -57,26 +57,62 @@ __device__ __forceinline__ int block_scan(int v, int* total)
     return before + x - v;
 }
 
-// What a place of a table needs before an append: 0 nothing, 1 a page, 2 a page with the
-// old one's contents.
-__device__ __forceinline__ int place_needs(int e, int64_t n_pages, const int32_t* ref, bool holds_tokens)
-{
-    if (e < 0 || e >= n_pages) return 1;
-    return __ldcg(ref + e) > 1 ? (holds_tokens ? 2 : 1) : 0;
-}
-
 }  // namespace
 
 struct PagesWork {
     PagesHead* head;
-    int32_t* claim;    // [batch] first fork of a target
-    int32_t* mark;     // [batch] target that is also a source, or holds pages
-    int32_t* count;    // [batch] pages a sequence needs, then the rank of its first
-    int32_t* free_id;  // [n_pages] free pages, lowest first
-    int32_t* drop;     // [n_pages] page a request leaves, or -1
-    int32_t* remap;    // [n_pages] new id of a page (compaction)
-    int2* moves;       // [max(batch, n_pages / 2 + 1)] (from, to)
+    int32_t* claim;     // [batch] first fork of a target
+    int32_t* mark;      // [batch] target that is also a source, or holds pages
+    int32_t* free_id;   // [n_pages] free pages, lowest first
+    uint32_t* place;    // [n_pages] requests in order: place in the table, bit 31: with the old page's contents
+    int32_t* drop;      // [n_pages] page a request leaves, or -1
+    int32_t* remap;     // [n_pages] new id of a page (compaction)
+    int2* moves;        // [max(batch, n_pages / 2 + 1)] (from, to)
 };
+
+namespace {
+
+// Entries of `n` rows of a table, four at a time per thread: load(row, column) of the four is
+// under way before use(row, column, value) of the first.
+template <typename Load, typename Use>
+__device__ __forceinline__ void for_entries(uint32_t n, uint32_t ld, Load load, Use use)
+{
+    const uint32_t total = n * ld;
+    for (uint32_t k0 = threadIdx.x; k0 < total; k0 += 4 * kPlanThreads) {
+        int v[4];
+        uint32_t row[4], col[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t k = k0 + u * kPlanThreads;
+            row[u] = k / ld;
+            col[u] = k - row[u] * ld;
+            v[u] = k < total ? load(row[u], col[u]) : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (k0 + u * kPlanThreads < total) use(row[u], col[u], v[u]);
+    }
+}
+
+// Eight counts from `base` on (a multiple of 8) as a mask of those that are 0; pages past the
+// end count as taken.
+__device__ __forceinline__ unsigned free_mask(const int32_t* ref, int base, int n_pages)
+{
+    int r[8];
+    if (base + 8 <= n_pages) {
+        const int4 a = __ldcg(reinterpret_cast<const int4*>(ref + base)), b = __ldcg(reinterpret_cast<const int4*>(ref + base) + 1);
+        r[0] = a.x, r[1] = a.y, r[2] = a.z, r[3] = a.w, r[4] = b.x, r[5] = b.y, r[6] = b.z, r[7] = b.w;
+    } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) r[u] = base + u < n_pages ? __ldcg(ref + base + u) : 1;
+    }
+    unsigned m = 0;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) m |= (unsigned)(r[u] <= 0) << u;
+    return m;
+}
+
+}  // namespace
 
 __global__ void __launch_bounds__(kPlanThreads)
 k_pages_update(int32_t* table, int32_t* ref, int batch, int table_ld, int page_tokens, int n_pages, int64_t kv_capacity,
@@ -85,102 +121,128 @@ k_pages_update(int32_t* table, int32_t* ref, int batch, int table_ld, int page_t
                const int32_t* __restrict__ len_after, PagesWork W, unsigned* status)
 {
     __shared__ int s_moves;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ int s_at[kPlanThreads], s_lo[kPlanThreads], s_lb[kPlanThreads];
+    const int tid = threadIdx.x;
     griddep_launch_dependents();   // the mover waits for this kernel's end before it reads anything
-
-    // ---- free: a place is emptied by whoever swaps its entry out, so a sequence may be named twice ----
-    for (int64_t k = tid; k < (int64_t)n_free * table_ld; k += kPlanThreads) {
-        const int s = __ldg(free_seq + k / table_ld);
-        if (s < 0 || s >= batch) {
-            set_status(status, QSA_DEV_BAD_SEQ);
-            continue;
-        }
-        const int e = atomicExch(table + (int64_t)s * table_ld + k % table_ld, -1);
-        if (e >= 0 && e < n_pages) atomicSub(ref + e, 1);
-    }
     if (tid == 0) s_moves = 0;
 
+    // ---- free: a place is emptied by whoever swaps its entry out, so a sequence may be named twice ----
+    for_entries(
+        n_free, table_ld,
+        [&](uint32_t f, uint32_t c) {
+            const int s = __ldg(free_seq + f);
+            if (s < 0 || s >= batch) {
+                set_status(status, QSA_DEV_BAD_SEQ);
+                return -1;
+            }
+            return atomicExch(table + (int64_t)s * table_ld + c, -1);
+        },
+        [&](uint32_t, uint32_t, int e) {
+            if (e >= 0 && e < n_pages) atomicSub(ref + e, 1);
+        });
+
     // ---- fork: a target counts once (its first fork), holds nothing and is nobody's source ----
-    auto fork_ok = [&](int f, int& src, int& dst) {
-        src = __ldg(fork_src + f);
-        dst = __ldg(fork_dst + f);
-        return src >= 0 && src < batch && dst >= 0 && dst < batch && src != dst;
-    };
     if (n_fork > 0) {
+        auto named = [&](int f, int& src, int& dst) {
+            src = __ldg(fork_src + f);
+            dst = __ldg(fork_dst + f);
+            return src >= 0 && src < batch && dst >= 0 && dst < batch && src != dst;
+        };
         int src, dst;
         for (int f = tid; f < n_fork; f += kPlanThreads)
-            if (fork_ok(f, src, dst)) {
+            if (named(f, src, dst)) {
                 W.claim[dst] = INT_MAX;
                 W.mark[dst] = 0;
+            } else {
+                set_status(status, QSA_DEV_BAD_SEQ);
             }
-        __syncthreads();
+        __syncthreads();   // the freed places are empty, too
         for (int f = tid; f < n_fork; f += kPlanThreads)
-            if (fork_ok(f, src, dst)) {
+            if (named(f, src, dst)) {
                 atomicMin(W.claim + dst, f);
                 W.mark[src] = 1;
             }
-        for (int64_t k = tid; k < (int64_t)n_fork * table_ld; k += kPlanThreads)
-            if (fork_ok((int)(k / table_ld), src, dst) && __ldcg(table + (int64_t)dst * table_ld + k % table_ld) >= 0)
-                W.mark[dst] = 1;
+        for_entries(
+            n_fork, table_ld,
+            [&](uint32_t f, uint32_t c) {
+                return named(f, src, dst) ? __ldcg(table + (int64_t)dst * table_ld + c) : -1;
+            },
+            [&](uint32_t f, uint32_t, int e) {
+                if (e >= 0) W.mark[__ldg(fork_dst + f)] = 1;
+            });
         __syncthreads();
-        for (int64_t k = tid; k < (int64_t)n_fork * table_ld; k += kPlanThreads) {
-            const int f = (int)(k / table_ld);
-            if (!fork_ok(f, src, dst) || __ldcg(W.claim + dst) != f || __ldcg(W.mark + dst) != 0) {
-                set_status(status, QSA_DEV_BAD_SEQ);
-                continue;
-            }
-            int e = __ldcg(table + (int64_t)src * table_ld + k % table_ld);
-            if (e >= n_pages) {
-                set_status(status, QSA_DEV_BAD_PAGE);
-                e = -1;
-            }
-            table[(int64_t)dst * table_ld + k % table_ld] = e;
-            if (e >= 0) atomicAdd(ref + e, 1);
-        }
+        for_entries(
+            n_fork, table_ld,
+            [&](uint32_t f, uint32_t c) {
+                return named(f, src, dst) ? __ldcg(table + (int64_t)src * table_ld + c) : -1;
+            },
+            [&](uint32_t f, uint32_t c, int e) {
+                if (!named(f, src, dst)) return;
+                if (__ldcg(W.claim + dst) != (int)f || __ldcg(W.mark + dst) != 0) {
+                    set_status(status, QSA_DEV_BAD_SEQ);
+                    return;
+                }
+                if (e >= n_pages) {
+                    set_status(status, QSA_DEV_BAD_PAGE);
+                    e = -1;
+                }
+                table[(int64_t)dst * table_ld + c] = e;
+                if (e >= 0) atomicAdd(ref + e, 1);
+            });
     }
     __syncthreads();
 
-    // ---- reserve, first pass: how many pages each sequence needs (a warp per sequence) ----
-    auto range = [&](int s, int& lo, int& hi, int& lb) {
-        lb = __ldg(len_before + s);
-        const int la = __ldg(len_after + s);
-        lo = hi = 0;
-        if (lb < 0 || la < lb || la > kv_capacity) return false;
-        if (la > lb) {
-            lo = lb / page_tokens;
-            hi = (la - 1) / page_tokens + 1;
-        }
-        return true;
-    };
-    for (int s = warp; s < batch; s += kPlanThreads / 32) {
-        int lo, hi, lb, n = 0;
-        if (!range(s, lo, hi, lb) && lane == 0) set_status(status, QSA_DEV_BAD_LEN);
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const int i = i0 + lane;
-            const bool need =
-                i < hi && place_needs(__ldcg(table + (int64_t)s * table_ld + i), n_pages, ref, (int64_t)i * page_tokens < lb);
-            n += __popc(__ballot_sync(0xffffffffu, need));
-        }
-        if (lane == 0) W.count[s] = n;
-    }
-    __syncthreads();
+    // ---- reserve: the places to fill, in the order of (sequence, place); 1,024 sequences at a time ----
     int wanted = 0;
     for (int s0 = 0; s0 < batch; s0 += kPlanThreads) {
         const int s = s0 + tid;
+        int lo = 0, n = 0, lb = 0;
+        if (s < batch) {
+            lb = __ldg(len_before + s);
+            const int la = __ldg(len_after + s);
+            if (lb < 0 || la < lb || la > kv_capacity) {
+                set_status(status, QSA_DEV_BAD_LEN);
+            } else if (la > lb) {
+                lo = lb / page_tokens;
+                n = (la - 1) / page_tokens + 1 - lo;
+            }
+        }
         int total;
-        const int at = block_scan(s < batch ? W.count[s] : 0, &total);
-        if (s < batch) W.count[s] = wanted + at;
-        wanted += total;   // at most the table's entries
+        s_at[tid] = block_scan(n, &total);
+        s_lo[tid] = lo;
+        s_lb[tid] = lb;
+        __syncthreads();
+        for (int c0 = 0; c0 < total; c0 += kPlanThreads) {
+            const int c = c0 + tid;
+            int needs = 0, e = -1;
+            uint32_t place = 0;
+            if (c < total) {
+                int t = 0;         // the last sequence that starts at or before candidate c
+#pragma unroll
+                for (int step = kPlanThreads / 2; step > 0; step >>= 1)
+                    if (s_at[t + step] <= c) t += step;
+                const int i = s_lo[t] + (c - s_at[t]);
+                place = (uint32_t)((int64_t)(s0 + t) * table_ld + i);
+                e = __ldcg(table + place);
+                if (e < 0 || e >= n_pages) e = -1, needs = 1;
+                else if (__ldcg(ref + e) > 1) needs = (int64_t)i * page_tokens < s_lb[t] ? 2 : 1;
+            }
+            int more;
+            const int rank = wanted + block_scan(needs != 0, &more);
+            if (needs != 0 && rank < n_pages) {
+                W.place[rank] = place | (needs == 2 ? 0x80000000u : 0u);
+                W.drop[rank] = e;
+            }
+            wanted += more;        // at most the table's entries
+        }
+        __syncthreads();
     }
 
     // ---- the lowest free pages ----
     int found = 0;
     for (int p0 = 0; p0 < n_pages && found < wanted; p0 += kPlanThreads * 8) {
-        unsigned mask = 0;
         const int base = p0 + tid * 8;
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (base + u < n_pages && __ldcg(ref + base + u) == 0) mask |= 1u << u;
+        const unsigned mask = base < n_pages ? free_mask(ref, base, n_pages) : 0u;
         int total;
         int at = found + block_scan(__popc(mask), &total);
 #pragma unroll
@@ -195,32 +257,16 @@ k_pages_update(int32_t* table, int32_t* ref, int batch, int table_ld, int page_t
     if (found < wanted && tid == 0) set_status(status, QSA_DEV_BAD_PAGE);
     __syncthreads();
 
-    // ---- second pass: the same decisions (counts of the pages looked at have not changed: a page
-    // taken here had none), requests served in order while there are pages ----
-    for (int s = warp; s < batch && found > 0; s += kPlanThreads / 32) {
-        int lo, hi, lb, at = W.count[s];
-        range(s, lo, hi, lb);
-        for (int i0 = lo; i0 < hi; i0 += 32) {
-            const int i = i0 + lane;
-            int32_t* place = table + (int64_t)s * table_ld + i;
-            const int e = i < hi ? __ldcg(place) : 0;
-            const int needs = i < hi ? place_needs(e, n_pages, ref, (int64_t)i * page_tokens < lb) : 0;
-            const unsigned who = __ballot_sync(0xffffffffu, needs != 0);
-            const int rank = at + __popc(who & ((1u << lane) - 1u));
-            at += __popc(who);
-            if (needs == 0 || rank >= found) continue;
-            const int to = W.free_id[rank];
-            W.drop[rank] = e >= 0 && e < n_pages ? e : -1;
-            if (needs == 2) W.moves[atomicAdd(&s_moves, 1)] = make_int2(e, to);
-            *place = to;
-        }
+    // ---- requests are served in order while there are pages ----
+    for (int r = tid; r < found; r += kPlanThreads) {
+        const uint32_t place = W.place[r];
+        const int to = W.free_id[r], old = W.drop[r];
+        table[place & 0x7FFFFFFFu] = to;
+        ref[to] = 1;               // it had no holder, so no count that was looked at changes
+        if (old >= 0) atomicSub(ref + old, 1);
+        if (place >> 31) W.moves[atomicAdd(&s_moves, 1)] = make_int2(old, to);
     }
     __syncthreads();
-    // ---- counts: pages taken have one holder, pages left one less ----
-    for (int r = tid; r < found; r += kPlanThreads) {
-        ref[W.free_id[r]] = 1;
-        if (W.drop[r] >= 0) atomicSub(ref + W.drop[r], 1);
-    }
     if (tid == 0) W.head->n_moves = s_moves;
 }
 
@@ -230,54 +276,53 @@ k_pages_compact(int32_t* ref, int n_pages, PagesWork W, int32_t* n_live_out)
     const int tid = threadIdx.x;
     griddep_launch_dependents();
     int n_live = 0;
+    unsigned first = 0;            // free pages of the first stretch, which the second pass needs again
     for (int p0 = 0; p0 < n_pages; p0 += kPlanThreads * 8) {
-        int n = 0;
         const int base = p0 + tid * 8;
-#pragma unroll
-        for (int u = 0; u < 8; ++u) n += base + u < n_pages && __ldcg(ref + base + u) > 0;
+        const unsigned mask = base < n_pages ? free_mask(ref, base, n_pages) : 0u;
+        if (p0 == 0) first = mask;
         int total;
-        block_scan(n, &total);
+        block_scan(base < n_pages ? min(8, n_pages - base) - __popc(mask) : 0, &total);
         n_live += total;
     }
     // k-th free id below n_live takes the k-th live id from n_live on: as many of one as of the other
     int holes = 0, movers = 0;
     for (int p0 = 0; p0 < n_pages; p0 += kPlanThreads * 8) {
-        unsigned mask = 0;
         const int base = p0 + tid * 8;
-        int n_hole = 0, n_move = 0;
+        const int n = base < n_pages ? min(8, n_pages - base) : 0;
+        const unsigned free = p0 == 0 ? first : n > 0 ? free_mask(ref, base, n_pages) : 0u;
+        unsigned hole = 0, move = 0;
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const int p = base + u;
-            if (p >= n_pages) continue;
-            const bool live = __ldcg(ref + p) > 0;
-            if (p < n_live ? !live : live) mask |= 1u << u;
-            if (p >= n_live && !live) W.remap[p] = -1;
+            if (u >= n) continue;
+            const bool is_free = free >> u & 1u;
+            if (base + u < n_live) hole |= (unsigned)is_free << u;
+            else if (is_free) W.remap[base + u] = -1;
+            else move |= 1u << u;
         }
+        // both counts of a stretch (8,192 at most) in one sum
+        int total;
+        const int at = block_scan(__popc(hole) | __popc(move) << 16, &total);
+        int ah = holes + (at & 0xFFFF), am = movers + (at >> 16);
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (mask >> u & 1u) (base + u < n_live ? n_hole : n_move)++;
-        int th, tm;
-        int ah = holes + block_scan(n_hole, &th), am = movers + block_scan(n_move, &tm);
-#pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (mask >> u & 1u) {
-                if (base + u < n_live) W.moves[ah++].y = base + u;
-                else W.moves[am++].x = base + u;
-            }
-        holes += th;
-        movers += tm;
-    }
-    __syncthreads();
-    for (int k = tid; k < holes; k += kPlanThreads) {
-        const int2 mv = W.moves[k];
-        W.remap[mv.x] = mv.y;
-        ref[mv.y] = ref[mv.x];
-        ref[mv.x] = 0;
+        for (int u = 0; u < 8; ++u) {
+            if (hole >> u & 1u) W.moves[ah++].y = base + u;
+            if (move >> u & 1u) W.moves[am++].x = base + u;
+        }
+        holes += total & 0xFFFF;
+        movers += total >> 16;
     }
     if (tid == 0) {
         W.head->n_moves = holes;
         W.head->n_live = n_live;
         *n_live_out = n_live;
+    }
+    __syncthreads();
+    for (int k = tid; k < holes; k += kPlanThreads) {
+        const int2 mv = W.moves[k];
+        W.remap[mv.x] = mv.y;
+        ref[mv.y] = __ldcg(ref + mv.x);
+        ref[mv.x] = 0;
     }
 }
 
@@ -340,8 +385,8 @@ size_t pages_layout(int batch, int64_t n_pages, char* ws, PagesWork* w)
     t.head = (PagesHead*)take(sizeof(PagesHead));
     t.claim = (int32_t*)take((size_t)batch * 4);
     t.mark = (int32_t*)take((size_t)batch * 4);
-    t.count = (int32_t*)take((size_t)batch * 4);
     t.free_id = (int32_t*)take((size_t)n_pages * 4);
+    t.place = (uint32_t*)take((size_t)n_pages * 4);
     t.drop = (int32_t*)take((size_t)n_pages * 4);
     t.remap = (int32_t*)take((size_t)n_pages * 4);
     t.moves = (int2*)take((size_t)moves * 8);
