@@ -84,7 +84,8 @@ struct __align__(1024) PromptSmem {
     uint64_t q_full[2], q_empty[2], kv_full[kRing], kv_empty[kRing];
     uint64_t s_full[2], p_full[2][2], o_full[2];   // P in two parts
     uint64_t v_full[kGuards], v_clean[kGuards];    // masked V tiles: landed, guarded
-    uint64_t item_full[kItems], item_empty[kItems], next_full, item_done, mma_done;
+    uint64_t item_full[kItems], item_empty[kItems], next_full, mma_done;
+    uint64_t tile_done[2];                         // a tile's epilogue is over
     uint32_t tmem_base;
     int error, any_bad;
 };
@@ -225,6 +226,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             mbar_init(&S.p_full[i][0], 4);                 // one arrival per softmax warp
             mbar_init(&S.p_full[i][1], 4);
             mbar_init(&S.o_full[i], 1);
+            mbar_init(&S.tile_done[i], 4);
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&S.kv_full[i], 1);
@@ -239,7 +241,6 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             mbar_init(&S.item_empty[i], kReaders);
         }
         mbar_init(&S.next_full, 1);
-        mbar_init(&S.item_done, 8);                        // one arrival per softmax warp
         mbar_init(&S.mma_done, 1);
         fence_mbar_init();
     }
@@ -441,19 +442,23 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         } else {
             // ---------------- V guard: 64 threads over the 32 KiB of each masked V tile ----------------
             const int gt = (warp - 2) * 32 + lane;
-            int k_ring = 0, n_mask = 0;
+            int k_ring = 0, n_mask = 0, n_done_b = 0;
+            bool had_b = false;
             Item it;
             for (int n = 0; read_item(n, it); ++n) {
                 const Tiles t = tiles_of(it);
-                // the last item's epilogues are done with `bad`
-                if (n > 0 && !wait_phase(&S.item_done, (n - 1) & 1, err, status)) break;
+                // the last item's epilogues are done with `bad`.  Each tile has its own count, of the
+                // items that have the tile: the warps of an absent B run ahead of A's
+                bool ok = n == 0 || wait_phase(&S.tile_done[0], (n - 1) & 1, err, status);
+                if (ok && had_b) ok = wait_phase(&S.tile_done[1], n_done_b++ & 1, err, status);
+                if (!ok) break;
+                had_b = t.n_b > 0;
                 if (*(volatile int*)&S.any_bad) {
                     asm volatile("bar.sync 1, 64;\n" ::: "memory");
                     for (int k = gt; k < 3 * kHeadDim; k += 64) (&S.bad[0][0])[k] = INT_MAX;
                     S.any_bad = 0;
                     asm volatile("bar.sync 1, 64;\n" ::: "memory");
                 }
-                bool ok = true;
                 for (int j = t.j_mask; j < t.n_kv && ok; ++j) {
                     const int g = n_mask++;
                     if (!(ok = wait_phase(&S.v_full[g % kGuards], (g / kGuards) & 1, err, status))) break;
@@ -643,9 +648,9 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                         }
                     }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S.tile_done[i]);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.item_done);
         }
     }
     tc_fence_before();

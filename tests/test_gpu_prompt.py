@@ -101,6 +101,26 @@ def test_many_sequences_are_found():
     _check(out, q, k, v, _cu(lens))
 
 
+@pytest.mark.parametrize("hq,hkv", [(16, 16), (8, 1)])
+def test_many_launches_of_prompts_with_and_without_second_tiles(hq, hkv):
+    """Items whose second query tile is absent, in a row and between long ones, launched back to
+    back: no wait runs out, and every launch gives the same bits."""
+    lens = [2, 359, 2, 6, 2, 18, 8, 6, 3, 9, 22, 3, 1951, 2, 147, 43, 6, 3, 6, 1, 54, 1]
+    q, k, v = _inputs(sum(lens), hq, hkv, 15)
+    first, flags = _run(q, k, v, _cu(lens))
+    assert flags == 0
+    _check(first, q, k, v, _cu(lens))
+    dims = qsa.make_dims(len(lens), hq, hkv, 8192)
+    cu = torch.tensor(_cu(lens), dtype=torch.int32, device="cuda")
+    outs = [torch.empty_like(first) for _ in range(4)]
+    ws = gu.new_workspace(256)
+    for i in range(4000):
+        qsa.qsa_prompt_attn(dims, q, k, v, cu, sum(lens), outs[i % 4], ws)
+    assert qsa.qsa_read_device_status(ws) == 0
+    for out in outs:
+        assert torch.equal(out, first)
+
+
 def test_fused_projection_slices_and_scale():
     q, k, v = _inputs(333, 8, 2, 7, fused=True)
     assert q.stride(0) == 12 * 128
