@@ -55,7 +55,7 @@ constexpr int kScales = kTok4 * kScaleRow;
 constexpr int kTile4 = 2 * (kCodes + kScales); // K codes, V codes, K scales, V scales
 constexpr int kItems4 = kSelCap + 2;           // selected blocks + up to 2 tail blocks
 constexpr int kItemCap4 = 576;                 // items of one split, in whole tiles
-constexpr int kMaxSplits4 = 16;                // one cluster
+constexpr int kMaxSplits4 = 8;                 // one cluster
 constexpr float kProbShift = 13.0f;            // probabilities are held times 2^13
 constexpr float kGrow4 = 2.0f;                 // growth of a row maximum (log2) that rescales the sums
 
@@ -720,18 +720,19 @@ Shape shape4(int nt, bool many)
 
 constexpr int kMaxArea = 160 * 1024;   // of the rings and merge buffers
 
+int shape_index(int nt, bool many) { return (nt == 1 ? 0 : nt == 2 ? 1 : 2) + (many ? 3 : 0); }
+
 bool configure4(int dev, int nt, bool many)
 {
     static std::atomic<bool> done[64][6];
-    const int ni = (nt == 1 ? 0 : nt == 2 ? 1 : 2) + (many ? 3 : 0);
     if (dev < 0 || dev >= 64) return false;
-    if (done[dev][ni].load()) return true;
+    std::atomic<bool>& d = done[dev][shape_index(nt, many)];
+    if (d.load()) return true;
     const Shape s = shape4(nt, many);
     if (cudaFuncSetAttribute(s.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             layout4(8 * nt, s.warps, s.depth, kMaxArea).total) != cudaSuccess ||
-        cudaFuncSetAttribute(s.fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+                             layout4(8 * nt, s.warps, s.depth, kMaxArea).total) != cudaSuccess)
         return false;
-    done[dev][ni].store(true);
+    d.store(true);
     return true;
 }
 
@@ -744,6 +745,44 @@ int area4(int rp, const Shape& s)
 
 }  // namespace
 
+// Splits of `pairs` lists: as many as still run all at once.  Clusters stay inside a group of
+// SMs (16 to 18 of them on a B200), so fewer fit than the SM count says: 8 splits of 16 pairs
+// took 15.0 us where 6 took 8.5 (8 query heads, one list of 2,048 tokens per pair); from 8
+// splits on (8.1 us for one pair) more of them gain nothing.  The device's answer per split
+// count is kept; without a device every SM counts.
+static int splits_at_once(int dev, int nt, int64_t pairs, const Shape& s, int smem)
+{
+    static std::atomic<int> fits[64][3][kMaxSplits4 + 1];   // clusters + 1; 0: not asked yet
+    for (int ns = kMaxSplits4; ns > 1; --ns) {
+        if (pairs * ns > 148) continue;
+        if (dev < 0 || dev >= 64) return ns;
+        std::atomic<int>& f = fits[dev][shape_index(nt, false)][ns];
+        int n = f.load();
+        if (n == 0) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)ns, 1, 1);
+            cfg.blockDim = dim3((unsigned)(32 * s.warps));
+            cfg.dynamicSmemBytes = (size_t)smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)ns;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int clusters = 0;
+            if (cudaOccupancyMaxActiveClusters(&clusters, s.fn, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                clusters = 0;
+            }
+            n = clusters + 1;
+            f.store(n);
+        }
+        if (n - 1 >= pairs) return ns;
+    }
+    return 1;
+}
+
 void plan_kv4(const qsa_dims& d, int64_t n_groups, int group_q, qsa_attn_plan_info* p)
 {
     const int rows = d.n_q_heads / d.n_kv_heads * group_q;
@@ -751,16 +790,21 @@ void plan_kv4(const qsa_dims& d, int64_t n_groups, int group_q, qsa_attn_plan_in
     const int64_t pairs = n_groups * d.n_kv_heads;
     const bool many = pairs >= 148;
     const Shape s = shape4(nt, many);
+    const int smem = layout4(rp, s.warps, s.depth, area4(rp, s)).total;
     const int ipt = kTok4 / d.block_size;
-    const int tiles_max = (kItems4 + ipt - 1) / ipt;
-    int ns = many ? 1 : (int)(148 / pairs > kMaxSplits4 ? kMaxSplits4 : 148 / pairs);
-    if (ns > tiles_max) ns = tiles_max;
+    const int tiles_max = (kItems4 + ipt - 1) / ipt;   // 17 to 257
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || !configure4(dev, nt, many)) {
+        cudaGetLastError();
+        dev = -1;
+    }
+    int ns = many ? 1 : splits_at_once(dev, nt, pairs, s, smem);
     const int tiles = (tiles_max + ns - 1) / ns;
     ns = (tiles_max + tiles - 1) / tiles;          // no split without a tile
     p->n_split = ns;
     p->n_stages = s.warps * s.depth;
     p->threads = 32 * s.warps;
-    p->smem_bytes = layout4(rp, s.warps, s.depth, area4(rp, s)).total;
+    p->smem_bytes = smem;
     p->ctas = pairs * ns;
     p->cluster_merge = ns > 1;
     p->rows = rows;
@@ -773,11 +817,8 @@ cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, co
     if (n_groups <= 0) return cudaSuccess;
     qsa_attn_plan_info p;
     plan_kv4(d, n_groups, group_q, &p);
-    int dev = 0;
-    cudaGetDevice(&dev);
     const int nt = nt_for(p.rows);
     const bool many = n_groups * d.n_kv_heads >= 148;
-    if (!configure4(dev, nt, many)) return cudaErrorInvalidValue;
     int bs_log2 = 0;
     while ((1 << bs_log2) < d.block_size) ++bs_log2;
     const int n_split = p.n_split, ipt = kTok4 >> bs_log2;
