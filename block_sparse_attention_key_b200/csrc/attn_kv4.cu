@@ -653,9 +653,11 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     auto store = [&](int row, int c, float4 a, float L) {
         if (row >= R) return;
         const float inv = L == 0.f ? 0.f : 1.f / L;   // a row that attends nothing is 0; a NaN sum stays NaN
-        uint2 v;
-        v.x = pack_bf16(a.x * inv, a.y * inv);
-        v.y = pack_bf16(a.z * inv, a.w * inv);
+        uint2 v = make_uint2(0u, 0u);                 // and so is one of a skipped query
+        if (s_rowt[row] >= 0) {
+            v.x = pack_bf16(a.x * inv, a.y * inv);
+            v.y = pack_bf16(a.z * inv, a.w * inv);
+        }
         *reinterpret_cast<uint2*>(out + ((qi0 + row / G) * n_q_heads + (int64_t)g * G + row % G) * kHeadDim + 4 * c) = v;
     };
     if (n_split == 1) {

@@ -186,12 +186,6 @@ def _check(fn, rc):
         raise QsaError(fn, rc, status_string(rc))
 
 
-# the calls behind torch.cuda.current_device() and current_stream(), without their wrappers' few
-# microseconds (a decode step's kernels take not many more)
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream
-
-
 def _ptr(t):
     if t is None:
         return None
@@ -207,7 +201,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    return _current_stream(_current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 # ---------------------------------------------------------------- entry points (same names as the C ABI)
@@ -300,6 +294,18 @@ def qsa_forward(dims, *, q, k_cache, v_cache, idx_k, pooled, q_idx, w, len_befor
 
 # ---------------------------------------------------------------- checked arguments of the serving operators
 
+# the calls behind torch.cuda.current_device() and current_stream(), without their wrappers' few
+# microseconds (a decode step's kernels take not many more); only used beside CUDA tensors
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_on(stream, dev):
+    if stream is None:
+        return _current_stream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _device_of(t):
     """Device index of a call's first tensor.  Launches go to the current device, so it has to be that."""
     dev = t.get_device()
@@ -355,7 +361,7 @@ def qsa_prompt_attn(dims, q, k, v, cu_len, n_tok, out, workspace=None, stream=No
     vp, v_ld = _rows_arg("v", v, n_tok, hkv, dev)
     args = qsa_prompt_args(qp, kp, vp, q_ld, k_ld, v_ld, _arg("cu_len", cu_len, torch.int32, (dims.batch + 1,), dev),
                            n_tok, _arg("out", out, torch.bfloat16, (n_tok, hq, 128), dev))
-    rc = load().qsa_prompt_attn(dims, args, _workspace_arg(workspace, dev), _stream(stream))
+    rc = load().qsa_prompt_attn(dims, args, _workspace_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_prompt_attn", rc)
 
@@ -408,7 +414,7 @@ def qsa_kv4_append(dims, cache, k, v, cu_len, len_before, n_tok, workspace=None,
     vp, v_ld = _rows_arg("v", v, n_tok, hkv, dev)
     rc = load().qsa_kv4_append(dims, cache, kp, k_ld, vp, v_ld, _arg("cu_len", cu_len, torch.int32, (batch + 1,), dev),
                                _arg("len_before", len_before, torch.int32, (batch,), dev), n_tok,
-                               _workspace_arg(workspace, dev), _stream(stream))
+                               _workspace_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_kv4_append", rc)
 
@@ -431,7 +437,7 @@ def qsa_sparse_attn_kv4(dims, cache, q, q_seq, q_pos, sel_idx, sel_cnt, n_q, out
                          _arg("sel_idx", sel_idx, i32, (groups, QSA_SEL_CAP), dev),
                          _arg("sel_cnt", sel_cnt, i32, (groups,), dev), n_q, group_q, None, 0, 0,
                          _arg("out", out, torch.bfloat16, rows, dev))
-    rc = load().qsa_sparse_attn_kv4(dims, cache, args, _workspace_arg(workspace, dev), _stream(stream))
+    rc = load().qsa_sparse_attn_kv4(dims, cache, args, _workspace_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_sparse_attn_kv4", rc)
 
@@ -484,7 +490,7 @@ def qsa_pages_update(dims, pools, page_table, page_ref, len_before, len_after, w
         dims, pools, table, ref, _list_arg("free_seq", free_seq, n_free, dev), n_free,
         _list_arg("fork_src", fork_src, n_fork, dev), _list_arg("fork_dst", fork_dst, n_fork, dev), n_fork,
         _arg("len_before", len_before, i32, batch, dev), _arg("len_after", len_after, i32, batch, dev),
-        _workspace_arg(workspace, dev), workspace.nbytes, _stream(stream))
+        _workspace_arg(workspace, dev), workspace.nbytes, _stream_on(stream, dev))
     if rc:
         _check("qsa_pages_update", rc)
 
@@ -494,7 +500,7 @@ def qsa_pages_compact(dims, pools, page_table, page_ref, n_live, workspace, stre
     dev = _device_of(page_table)
     table, ref = _page_state(dims, pools, page_table, page_ref, dev)
     rc = load().qsa_pages_compact(dims, pools, table, ref, _arg("n_live", n_live, torch.int32, (1,), dev),
-                                  _workspace_arg(workspace, dev), workspace.nbytes, _stream(stream))
+                                  _workspace_arg(workspace, dev), workspace.nbytes, _stream_on(stream, dev))
     if rc:
         _check("qsa_pages_compact", rc)
 

@@ -370,6 +370,45 @@ def test_bad_indices_are_reported_and_skipped():
     _attend(c, f.QSA_DEV_BAD_PAGE)
 
 
+def test_skipped_drafts_are_zero_and_leave_the_others_alone():
+    """A draft of another sequence, before its group or too far behind it, beside valid ones."""
+    f = qsa.qsa
+    for ns, t0s in ((1, [1501]), (40, [1501] * 40)):       # split over a cluster, one CTA per pair
+        c = _case(2, 16, 4, 2048, 0, 4, 512, 4, t0s, 13)
+        good = _attend(c)
+        _compare(c, good, rows=range(4))
+        for field, val, bit in (("q_seq", 1, f.QSA_DEV_BAD_SEQ), ("q_pos", 1500, f.QSA_DEV_BAD_POS),
+                                ("q_pos", 1508, f.QSA_DEV_BAD_POS)):
+            keep = c[field].clone()
+            c[field][2] = val
+            out = _attend(c, bit)
+            c[field] = keep
+            assert (out[2] == 0).all()
+            rest = [i for i in range(out.shape[0]) if i != 2]
+            assert torch.equal(out[rest], good[rest])
+
+
+def test_two_streams_and_a_graph_at_once():
+    """Calls that overlap on the GPU share nothing."""
+    cases = [_case(3, 32, 4, 2304, page, 4, 512, 1, [2000, 900, 2200], 20 + page) for page in (0, 16)]
+    want = [_attend(c) for c in cases]
+    outs = [torch.empty_like(w) for w in want]
+
+    def call(i, **kw):
+        c = cases[i]
+        qsa.qsa_sparse_attn_kv4(c["dims"], c["cache"], c["q"], c["q_seq"], c["q_pos"], c["sel"], c["cnt"], 3, outs[i], **kw)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    side = torch.cuda.Stream()
+    for _ in range(50):
+        graph.replay()
+        call(1, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
 def test_drafts_do_not_see_what_lies_behind_them():
     """A tail token that is not finite reaches the drafts at and behind it only."""
     c = _case(1, 8, 2, 512, 0, 4, 512, 4, [301], 6)        # drafts at 301..304, tail from 300

@@ -228,6 +228,20 @@ def test_full_empty_and_single_page_pools_compact():
     one.compact()
 
 
+def test_more_sequences_and_longer_ranges_than_a_pass_covers():
+    """1,500 sequences (scanned 1,024 at a time), one of them reserving 2,900 pages at once."""
+    p = Pool(1500, 3000, 6000, 1, widths=(16,))
+    after = [2] * 1500
+    after[1200] = 2900
+    assert p.update([], [], [0] * 1500, after) == 0
+    free = [s for s in range(1500) if s % 3 == 0]
+    assert p.update(free, [(1, 0), (1200, 3)], [0] * 1500, [0] * 1500) == 0
+    before = [0 if s % 3 == 0 else 2 for s in range(1500)]
+    before[0], before[3], before[1200] = 2, 2900, 0
+    assert p.update([], [], before, [min(n + 1, 3000) if n else 0 for n in before]) == 0
+    p.compact()
+
+
 def test_large_pools_and_odd_page_sizes_move_whole():
     """Pages of 33,168 bytes (not a whole number of steps) beside ones of 16, over 20,000 pages."""
     p = Pool(64, 500, 20000, 1, widths=(16,))

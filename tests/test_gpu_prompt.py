@@ -206,6 +206,32 @@ def test_captured_and_replayed_on_another_stream_with_new_lengths():
     assert (out[390:] == 77).all()
 
 
+def test_two_streams_at_once():
+    data = [_inputs(900, 8, 2, 30 + i) for i in range(2)]
+    cu = torch.tensor([0, 300, 900], dtype=torch.int32, device="cuda")
+    dims = qsa.make_dims(2, 8, 2, 8192)
+    want = [_run(*d, [0, 300, 900])[0] for d in data]
+    outs = [torch.empty_like(w) for w in want]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for d, out, st in zip(data, outs, streams):
+            qsa.qsa_prompt_attn(dims, *d, cu, 900, out, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+
+
+def test_output_that_is_aligned_to_16_bytes_only():
+    q, k, v = _inputs(150, 8, 1, 16)
+    want, _ = _run(q, k, v, [0, 150])
+    flat = torch.full((150 * 8 * 128 + 16,), 77.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[8:-8].view(150, 8, 128)
+    assert out.data_ptr() % 32 == 16
+    got, flags = _run(q, k, v, [0, 150], out=out)
+    assert flags == 0 and torch.equal(got, want)
+    assert (flat[:8] == 77).all() and (flat[-8:] == 77).all()
+
+
 def test_same_inputs_give_the_same_bits():
     q, k, v = _inputs(1000, 16, 2, 13)
     a, _ = _run(q, k, v, [0, 400, 1000])
