@@ -489,7 +489,11 @@ int qsa_forward(const qsa_dims* dims, const qsa_forward_args* a, void* workspace
 static int check_kv4(const qsa_dims* d, const qsa_kv4_cache* c)
 {
     if (!c) return QSA_ERR_INVALID_ARG;
-    return check_pages(d, c->page_table, c->page_tokens, c->n_pages);
+    const int rc = check_pages(d, c->page_table, c->page_tokens, c->n_pages);
+    if (rc != QSA_OK) return rc;
+    // token rows (64 bytes of codes each: 256 GiB) are counted in 32 bits, all ones for none
+    const int64_t tokens = c->page_table ? c->n_pages * c->page_tokens : d->batch * d->kv_capacity;
+    return tokens > 0xFFFFFFFEll / d->n_kv_heads ? QSA_ERR_UNSUPPORTED : QSA_OK;
 }
 
 static bool kv4_aligned(const qsa_kv4_cache* c)

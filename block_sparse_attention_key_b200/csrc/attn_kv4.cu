@@ -55,6 +55,7 @@ constexpr int kScales = kTok4 * kScaleRow;
 constexpr int kTile4 = 2 * (kCodes + kScales); // K codes, V codes, K scales, V scales
 constexpr int kItems4 = kSelCap + 2;           // selected blocks + up to 2 tail blocks
 constexpr int kItemCap4 = 576;                 // items of one split, in whole tiles
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;       // no such token row (a cache has fewer: the host checks)
 constexpr int kMaxSplits4 = 8;                 // one cluster
 constexpr float kProbShift = 13.0f;            // probabilities are held times 2^13
 constexpr float kGrow4 = 2.0f;                 // growth of a row maximum (log2) that rescales the sums
@@ -70,7 +71,7 @@ __host__ __device__ inline Layout4 layout4(int rp, int warps, int depth, int are
     L.ring = rp * kHeadDim * 2;
     L.tok = L.ring + area;
     L.ioff = L.tok + warps * depth * kTok4 * 4;
-    L.ipos = L.ioff + kItemCap4 * 8;
+    L.ipos = L.ioff + kItemCap4 * 4;
     L.rowt = L.ipos + kItemCap4 * 4;
     L.rows = L.rowt + 32 * 4;
     L.total = L.rows + 32 * 4;
@@ -199,7 +200,7 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     __shared__ int s_cnt, s_nitems, s_seq, s_nc0, s_tlast;
     const Layout4 SL = layout4(RP, KW, D, area);
     const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
-    long long* s_ioff = reinterpret_cast<long long*>(smem + SL.ioff);
+    uint32_t* s_ioff = reinterpret_cast<uint32_t*>(smem + SL.ioff);
     int* s_ipos = reinterpret_cast<int*>(smem + SL.ipos);
     int* s_rowt = reinterpret_cast<int*>(smem + SL.rowt);
     float* s_rows = reinterpret_cast<float*>(smem + SL.rows);
@@ -303,16 +304,16 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
             p0 = (nc0 + (a - cnt)) << bs_log2;
             ipos = p0;
         }
-        long long off = -1;      // token row in the cache
+        uint32_t off = kNoRow;   // token row in the cache
         if (p0 >= 0) {
             if (page_table) {
                 const int page = __ldg(page_table + (int64_t)s * table_ld + p0 / page_tokens);
                 if (page >= 0 && page < n_pages)
-                    off = ((long long)page * n_kv_heads + g) * page_tokens + p0 % page_tokens;
+                    off = ((uint32_t)page * n_kv_heads + g) * page_tokens + p0 % page_tokens;
                 else
                     set_status(status, QSA_DEV_BAD_PAGE);
             } else {
-                off = ((long long)s * n_kv_heads + g) * kv_capacity + p0;
+                off = ((uint32_t)s * n_kv_heads + g) * (uint32_t)kv_capacity + p0;
             }
         }
         s_ioff[k] = off;
@@ -323,6 +324,7 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     const int tlast = s_tlast;
     const int n_tiles = (n_blk + ipt - 1) / ipt;
     const uint32_t ring = sbase + SL.ring + warp * (D * kTile4);
+    const uint8_t *k_lane = k_codes + (lane & 3) * 16, *v_lane = v_codes + (lane & 3) * 16;
     int* s_tok = reinterpret_cast<int*>(smem + SL.tok) + warp * (D * kTok4);
     // One tile into a slot of the warp's ring; returns whether some token of it is absent or
     // not visible to every row (then the tokens' positions are in s_tok).
@@ -330,31 +332,41 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         const uint32_t st = ring + slot * kTile4;
         // lane = token row: its place in the cache, its scales
         const int it = tile * ipt + (lane >> bs_log2), tin = lane & (bs - 1);
-        long long e = -1;
+        uint32_t e = kNoRow;
         int tp = INT_MAX;
         if (it < n_blk) {
             e = s_ioff[it];
             const int ip = s_ipos[it];
-            if (ip >= 0 && ip + tin > tlast) e = -1;       // past the group's last draft token
-            if (e >= 0) {
+            if (ip >= 0 && ip + tin > tlast) e = kNoRow;   // past the group's last draft token
+            if (e != kNoRow) {
                 e += tin;
                 tp = ip < 0 ? -1 : ip + tin;
             }
         }
-        const long long es = e >= 0 ? e : 0;
-        cp_async8(st + 2 * kCodes + lane * 8, k_scales + es * kScaleRow, e >= 0 ? 8 : 0);
-        cp_async8(st + 2 * kCodes + kScales + lane * 8, v_scales + es * kScaleRow, e >= 0 ? 8 : 0);
         // four lanes per row, a 16-byte chunk of K and of V codes each; the upper bit of V's
         // chunk is flipped every two tokens, so that the reads below meet no bank twice
-        const int q4 = lane & 3;
+        const uint32_t kd = st + (lane >> 2) * 64 + (lane & 3) * 16;
+        const uint32_t vd = st + kCodes + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 2) & 2)) << 4);
+        auto copy = [&](uint32_t row, int u, int n16) {
+            const uint64_t at = (uint64_t)row * kCodeRow;
+            cp_async16(kd + 512 * u, k_lane + at, n16);
+            cp_async16(vd + 512 * u, v_lane + at, n16);
+        };
+        if (__all_sync(0xffffffffu, e != kNoRow)) {
+            cp_async8(st + 2 * kCodes + lane * 8, k_scales + (uint64_t)e * kScaleRow, 8);
+            cp_async8(st + 2 * kCodes + kScales + lane * 8, v_scales + (uint64_t)e * kScaleRow, 8);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int row = (lane >> 2) + 8 * u;
-            const long long er = __shfl_sync(0xffffffffu, e, row);
-            const long long src = (er >= 0 ? er : 0) * kCodeRow + q4 * 16;
-            const int n16 = er >= 0 ? 16 : 0;
-            cp_async16(st + row * 64 + q4 * 16, k_codes + src, n16);
-            cp_async16(st + kCodes + row * 64 + ((q4 ^ (row & 2)) << 4), v_codes + src, n16);
+            for (int u = 0; u < 4; ++u) copy(__shfl_sync(0xffffffffu, e, (lane >> 2) + 8 * u), u, 16);
+        } else {
+            // absent tokens are filled with zeros
+            const uint64_t es = e != kNoRow ? e : 0u;
+            cp_async8(st + 2 * kCodes + lane * 8, k_scales + es * kScaleRow, e != kNoRow ? 8 : 0);
+            cp_async8(st + 2 * kCodes + kScales + lane * 8, v_scales + es * kScaleRow, e != kNoRow ? 8 : 0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint32_t er = __shfl_sync(0xffffffffu, e, (lane >> 2) + 8 * u);
+                copy(er != kNoRow ? er : 0u, u, er != kNoRow ? 16 : 0);
+            }
         }
         cp_commit();
         const bool special = __any_sync(0xffffffffu, tp != -1);
@@ -407,6 +419,10 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     // (K's reads), the even rows are tokens 0 to 3 (V's reads)
     const int tk = l4 & 1 ? 4 + ((l4 >> 1) ^ 1) : l4 >> 1;
     const int tv0 = c4, tv1 = 4 + (c4 ^ 1);   // of rows 2 c4 and 2 c4 + 1
+    const uint32_t k_at = tk * 64 + c4 * 16, ks_at = 2 * kCodes + tk * 8 + 2 * c4;
+    const uint32_t v_at = kCodes + (((l4 >> 1) ^ (c4 & 2)) << 4) + (l4 & 1) * 8, vs_at = 2 * kCodes + kScales + l4;
+    const uint32_t v_at0 = v_at + tv0 * 64, v_at1 = v_at + tv1 * 64;   // (tv0 and tv1 have the same bit 1)
+    const uint32_t vs_at0 = vs_at + tv0 * 8, vs_at1 = vs_at + tv1 * 8;
 
     int slot = 0;
     for (int t = warp; t < n_tiles; t += KW) {
@@ -422,10 +438,8 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[h][nt][e] = 0.f;
-            const uint32_t kr = st + (16 * h + tk) * 64 + c4 * 16;
-            const uint4 k0 = lds128(kr), k1 = lds128(kr + 512);
-            const uint32_t ksc = st + 2 * kCodes + (16 * h + tk) * 8 + 2 * c4;
-            const uint32_t s0 = unpack_e4m3x2(lds16(ksc)), s1 = unpack_e4m3x2(lds16(ksc + 64));
+            const uint4 k0 = lds128(st + k_at + 1024 * h), k1 = lds128(st + k_at + 1024 * h + 512);
+            const uint32_t s0 = unpack_e4m3x2(lds16(st + ks_at + 128 * h)), s1 = unpack_e4m3x2(lds16(st + ks_at + 128 * h + 64));
             const uint32_t kw0[4] = {k0.x, k0.y, k0.z, k0.w}, kw1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -525,11 +539,11 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
             uint32_t vs[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int tt = 16 * h + (u & 1 ? tv1 : tv0) + (u & 2 ? 8 : 0);
-                vw[u] = lds64(st + kCodes + tt * 64 + (((l4 >> 1) ^ (tt & 2)) << 4) + (l4 & 1) * 8);
-                vs[u] = lds8(st + 2 * kCodes + kScales + tt * 8 + l4);
+                const int rows = 16 * h + (u & 2 ? 8 : 0);
+                vw[u] = lds64(st + (u & 1 ? v_at1 : v_at0) + rows * 64);
+                vs[u] = lds8(st + (u & 1 ? vs_at1 : vs_at0) + rows * 8);
                 if (masked && group_q > 1) {
-                    const int tp = s_tok[slot * kTok4 + tt];
+                    const int tp = s_tok[slot * kTok4 + rows + (u & 1 ? tv1 : tv0)];
                     if (tp >= 0 && tp != INT_MAX && (vs[u] & 0x7Fu) == 0x7Fu) {
                         bad = min(bad, tp);
                         vs[u] = 0;

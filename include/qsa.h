@@ -314,7 +314,8 @@ int qsa_forward(const qsa_dims* dims, const qsa_forward_args* args, void* worksp
  * (72 bytes instead of 256).  Codes and scales are separate arrays, each laid out like the
  * bf16 caches with 64 or 8 bytes in the place of the 128 values: [batch][n_kv_heads]
  * [kv_capacity][64 | 8], or with page_table != NULL pools [n_pages][n_kv_heads]
- * [page_tokens][64 | 8] (see qsa_sparse_attn_ex).  All pointers 16-byte aligned.  The
+ * [page_tokens][64 | 8] (see qsa_sparse_attn_ex), fewer than 2^32 - 1 token rows in all.
+ * All pointers 16-byte aligned.  The
  * indexer's keys and the pooled cache stay as they are. */
 typedef struct qsa_kv4_cache {
     void* k_codes;              /* u8 */
