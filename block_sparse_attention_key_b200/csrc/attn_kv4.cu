@@ -17,7 +17,7 @@
 // query heads of that KV head (<= 32), tokens on the M side of mma.sync m16n8k16.  The
 // splits of a (group, KV head) form one thread-block cluster and read one another's partials
 // through shared memory, each finishing a share of the rows, so a call needs no scratch.  What differs from a bf16 gather is that
-// unpacking, not the copies, is the work (about 500 instructions per warp and 32 tokens,
+// unpacking, not the copies, is the work (about 700 instructions per warp and 32 tokens,
 // 2.3 KB of each K and V), so operands never pass through shared memory unpacked and
 // warps do not wait for one another: each takes 32 tokens at a time through a ring of its
 // own (cp.async, four lanes per row of codes), and only the end is a block's.
@@ -29,6 +29,11 @@
 // (4 logic operations per 16 values).  The running maximum moves when it grew by more
 // than 2 (probabilities then reach 2^16 / 2, inside fp16), so accumulators are rescaled
 // in few steps.
+//
+// Measured: 1,024 queries of 2,052 tokens at 32 / 4 heads 271 us (ALU pipe two thirds busy: one
+// conversion per two values is what the format costs); a decode step of 16 x 64K contexts
+// 11.6 us (18.9 MB), of one 8K context with two drafts 9.8 us: round trips and one pass
+// through code that is not in the instruction cache yet.
 //
 // Masked places: absent tokens are zero-filled and their logits -inf.  A scale may be NaN
 // (the append writes that for values that are not finite): a draft's tail token that is
@@ -720,31 +725,46 @@ namespace {
 
 int nt_for(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
-// One kernel per row tile count and call shape.  Few pairs: one CTA per SM, as many warps as
-// its registers allow; many pairs: smaller CTAs, several per SM.
+// One kernel per row tile count and call size (lists = query groups x KV heads).  Few lists:
+// one CTA per SM (or a cluster per list), as many warps as its registers allow.  More: smaller
+// CTAs, several per SM, whose starts and ends overlap and whose last wave is shorter.  Lists of
+// 2,052 tokens, us:
+//   <= 8 rows, 16 / 8 / 4 / 2 warps: 148 lists 15.6 / 17.2 / 23.1 / 40, 296 lists 29.4 / 25.2 /
+//   28.5 / 41, 400 lists 42.1 / 37.5 / 36.2 / 50, 4,096 lists 371 / 292 / 271 / 268
+//   <= 16 rows, 8 / 4 / 2 warps: 148 lists 23.0 / 30.2 / 45.2, 200 lists 43.1 / 36.4 / 45.9,
+//   2,368 lists 333 / 232 / 233
+//   <= 32 rows, 8 / 4 / 2 warps: 148 lists 33.3 / 42.0 / 72.5, 200 lists 62.4 / 53.8 / 74.5,
+//   400 lists 93 / 100 / 98, 2,368 lists 488 / 409 / 387
+int tier4(int64_t lists) { return lists <= 148 ? 0 : lists <= 296 ? 1 : 2; }
+
 struct Shape {
     const void* fn;
     int warps, depth;
 };
-Shape shape4(int nt, bool many)
+Shape shape4(int nt, int tier)
 {
     if (nt == 1)
-        return many ? Shape{(const void*)k_sparse_attn_kv4<1, 8, 2>, 8, 2} : Shape{(const void*)k_sparse_attn_kv4<1, 16, 2>, 16, 2};
-    if (nt == 2) return Shape{(const void*)k_sparse_attn_kv4<2, 8, 2>, 8, 2};
-    return Shape{(const void*)k_sparse_attn_kv4<4, 8, 2>, 8, 2};
+        return tier == 0   ? Shape{(const void*)k_sparse_attn_kv4<1, 16, 2>, 16, 2}
+               : tier == 1 ? Shape{(const void*)k_sparse_attn_kv4<1, 8, 2>, 8, 2}
+                           : Shape{(const void*)k_sparse_attn_kv4<1, 4, 2>, 4, 2};
+    if (nt == 2)
+        return tier == 0 ? Shape{(const void*)k_sparse_attn_kv4<2, 8, 2>, 8, 2}
+                         : Shape{(const void*)k_sparse_attn_kv4<2, 4, 2>, 4, 2};
+    return tier == 0 ? Shape{(const void*)k_sparse_attn_kv4<4, 8, 2>, 8, 2}
+                     : Shape{(const void*)k_sparse_attn_kv4<4, 4, 2>, 4, 2};
 }
 
 constexpr int kMaxArea = 160 * 1024;   // of the rings and merge buffers
 
-int shape_index(int nt, bool many) { return (nt == 1 ? 0 : nt == 2 ? 1 : 2) + (many ? 3 : 0); }
+int shape_index(int nt, int tier) { return (nt == 1 ? 0 : nt == 2 ? 1 : 2) + 3 * tier; }
 
-bool configure4(int dev, int nt, bool many)
+bool configure4(int dev, int nt, int tier)
 {
-    static std::atomic<bool> done[64][6];
+    static std::atomic<bool> done[64][9];
     if (dev < 0 || dev >= 64) return false;
-    std::atomic<bool>& d = done[dev][shape_index(nt, many)];
+    std::atomic<bool>& d = done[dev][shape_index(nt, tier)];
     if (d.load()) return true;
-    const Shape s = shape4(nt, many);
+    const Shape s = shape4(nt, tier);
     if (cudaFuncSetAttribute(s.fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              layout4(8 * nt, s.warps, s.depth, kMaxArea).total) != cudaSuccess)
         return false;
@@ -804,17 +824,17 @@ void plan_kv4(const qsa_dims& d, int64_t n_groups, int group_q, qsa_attn_plan_in
     const int rows = d.n_q_heads / d.n_kv_heads * group_q;
     const int nt = nt_for(rows), rp = 8 * nt;
     const int64_t pairs = n_groups * d.n_kv_heads;
-    const bool many = pairs >= 148;
-    const Shape s = shape4(nt, many);
+    const int tier = tier4(pairs);
+    const Shape s = shape4(nt, tier);
     const int smem = layout4(rp, s.warps, s.depth, area4(rp, s)).total;
     const int ipt = kTok4 / d.block_size;
     const int tiles_max = (kItems4 + ipt - 1) / ipt;   // 17 to 257
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess || !configure4(dev, nt, many)) {
+    if (cudaGetDevice(&dev) != cudaSuccess || !configure4(dev, nt, tier)) {
         cudaGetLastError();
         dev = -1;
     }
-    int ns = many ? 1 : splits_at_once(dev, nt, pairs, s, smem);
+    int ns = tier > 0 ? 1 : splits_at_once(dev, nt, pairs, s, smem);
     const int tiles = (tiles_max + ns - 1) / ns;
     ns = (tiles_max + tiles - 1) / tiles;          // no split without a tile
     p->n_split = ns;
@@ -834,13 +854,13 @@ cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, co
     qsa_attn_plan_info p;
     plan_kv4(d, n_groups, group_q, &p);
     const int nt = nt_for(p.rows);
-    const bool many = n_groups * d.n_kv_heads >= 148;
+    const int tier = tier4(n_groups * d.n_kv_heads);
     int bs_log2 = 0;
     while ((1 << bs_log2) < d.block_size) ++bs_log2;
     const int n_split = p.n_split, ipt = kTok4 >> bs_log2;
     const int tiles_max = (kItems4 + ipt - 1) / ipt;
     const int items = (tiles_max + n_split - 1) / n_split * ipt;   // of one split, in whole tiles
-    const int area = area4(8 * nt, shape4(nt, many));
+    const int area = area4(8 * nt, shape4(nt, tier));
     const float scale = d.softmax_scale > 0.f ? d.softmax_scale : 1.0f / sqrtf((float)d.head_dim);
 
     cudaLaunchConfig_t cfg = {};
@@ -864,8 +884,12 @@ cudaError_t launch_sparse_attn_kv4(const qsa_dims& d, const qsa_kv4_cache& c, co
             (int)d.n_q_heads, (int)d.n_kv_heads, d.kv_capacity, bs_log2, (int)d.top_k, group_q,
             scale * 1.4426950408889634f, items, n_split, area, (__nv_bfloat16*)out, status);
     };
-    if (nt == 1) return many ? go(k_sparse_attn_kv4<1, 8, 2>) : go(k_sparse_attn_kv4<1, 16, 2>);
-    return nt == 2 ? go(k_sparse_attn_kv4<2, 8, 2>) : go(k_sparse_attn_kv4<4, 8, 2>);
+    if (nt == 1)
+        return tier == 0   ? go(k_sparse_attn_kv4<1, 16, 2>)
+               : tier == 1 ? go(k_sparse_attn_kv4<1, 8, 2>)
+                           : go(k_sparse_attn_kv4<1, 4, 2>);
+    if (nt == 2) return tier == 0 ? go(k_sparse_attn_kv4<2, 8, 2>) : go(k_sparse_attn_kv4<2, 4, 2>);
+    return tier == 0 ? go(k_sparse_attn_kv4<4, 8, 2>) : go(k_sparse_attn_kv4<4, 4, 2>);
 }
 
 }  // namespace qsa

@@ -284,8 +284,18 @@ def test_query_counts_from_split_rows_to_chunks(n, hq, hkv):
     """One query up to a chunk: split lists merged in a cluster, then one CTA per pair."""
     g = torch.Generator().manual_seed(n)
     t0s = torch.randint(0, 3000, (n,), generator=g).tolist()
-    c = _case(2, hq, hkv, 3072, 0, 4, 512, 1, t0s, n)
+    c = _case(2, hq, hkv, 3200, 0, 4, 512, 1, t0s, n)
     _compare(c, _attend(c), rows=range(0, n, max(1, n // 25)))
+
+
+@pytest.mark.parametrize("lists", [148, 149, 296, 297])
+@pytest.mark.parametrize("hq,group", [(4, 2), (16, 1), (16, 2), (11, 2)])
+def test_every_launch_shape(hq, group, lists):
+    """Row tiles of 8, 16 and 32 in the CTAs of few, of some and of many lists."""
+    g = torch.Generator().manual_seed(lists + hq)
+    t0s = torch.randint(0, 2300, (lists,), generator=g).tolist()
+    c = _case(2, hq, 1, 2304, 16, 4, 512, group, t0s, lists * hq)
+    _compare(c, _attend(c), rows=range(0, lists * group, 13))
 
 
 def test_every_code_and_scale_reads_as_its_value():

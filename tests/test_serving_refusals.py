@@ -188,7 +188,7 @@ def test_kv4_plans_fit_the_hardware(qsa):
     empty, merge buffers and stages fit 227 KB (an independent restatement of the layout)."""
     import itertools
     import math
-    for rows, bs, pairs in itertools.product((1, 8, 9, 16, 17, 32), (1, 2, 4, 8, 16), (1, 2, 3, 7, 9, 16, 37, 64, 100, 147, 148, 5000)):
+    for rows, bs, pairs in itertools.product((1, 8, 9, 16, 17, 32), (1, 2, 4, 8, 16), (1, 2, 3, 7, 9, 16, 37, 64, 100, 147, 148, 149, 296, 297, 5000)):
         rp = 8 if rows <= 8 else 16 if rows <= 16 else 32
         d = qsa.make_dims(1, rows, 1, 65536, block_size=bs)
         info = qsa.qsa_attn_plan_info()
