@@ -39,6 +39,12 @@
 //                exponentials, P back to TMEM in two parts (the MMA starts on the first);
 //                at the end O / l to global memory, 32 bytes per store.
 // Every wait is bounded (QSA_DEV_TIMEOUT, drain, free TMEM, return).
+//
+// Measured: 8,192 tokens at 32 / 4 heads 443 us (1,240 TFLOP/s, 0.75 of a cuBLAS product's
+// burst rate; tensor and special-function pipes 60% busy each).  A step of 128 keys and 256
+// rows takes 3,200 cycles, 2,048 of them tensor time: a tile's S waits for its own P to be
+// read, since TMEM has no room for a second S.  16 ragged prompts (5,824 tokens, 16 / 16
+// heads) 48 us, 122 tokens 9.3 us.
 
 #include <atomic>
 #include <climits>

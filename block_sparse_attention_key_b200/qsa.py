@@ -294,6 +294,7 @@ def qsa_forward(dims, *, q, k_cache, v_cache, idx_k, pooled, q_idx, w, len_befor
 
 # ---------------------------------------------------------------- checked arguments of the serving operators
 
+_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
 # the calls behind torch.cuda.current_device() and current_stream(), without their wrappers' few
 # microseconds (a decode step's kernels take not many more); only used beside CUDA tensors
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
@@ -329,7 +330,7 @@ def _arg(name, t, dtype, shape, dev):
 
 def _rows_arg(name, t, n_tok, heads, dev):
     """Pointer and token stride of bf16 [n_tok][heads][128], heads dense, tokens at any stride."""
-    if t.dtype is not torch.bfloat16 or t.shape != (n_tok, heads, 128):
+    if t.dtype is not _BF16 or t.shape != (n_tok, heads, 128):
         raise ValueError(f"{name}: torch.bfloat16 {(n_tok, heads, 128)} expected, got {t.dtype} {tuple(t.shape)}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: tensor on {t.device}, but the current device is cuda:{dev}")
@@ -359,9 +360,9 @@ def qsa_prompt_attn(dims, q, k, v, cu_len, n_tok, out, workspace=None, stream=No
     qp, q_ld = _rows_arg("q", q, n_tok, hq, dev)
     kp, k_ld = _rows_arg("k", k, n_tok, hkv, dev)
     vp, v_ld = _rows_arg("v", v, n_tok, hkv, dev)
-    args = qsa_prompt_args(qp, kp, vp, q_ld, k_ld, v_ld, _arg("cu_len", cu_len, torch.int32, (dims.batch + 1,), dev),
-                           n_tok, _arg("out", out, torch.bfloat16, (n_tok, hq, 128), dev))
-    rc = load().qsa_prompt_attn(dims, args, _workspace_arg(workspace, dev), _stream_on(stream, dev))
+    args = qsa_prompt_args(qp, kp, vp, q_ld, k_ld, v_ld, _arg("cu_len", cu_len, _I32, (dims.batch + 1,), dev),
+                           n_tok, _arg("out", out, _BF16, (n_tok, hq, 128), dev))
+    rc = (_lib or load()).qsa_prompt_attn(dims, args, _workspace_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_prompt_attn", rc)
 
@@ -378,7 +379,7 @@ def kv4_cache(k_codes, k_scales, v_codes, v_scales, page_table=None, page_tokens
     dev = k_codes.get_device()
     if dev < 0:
         raise ValueError("libqsa takes CUDA tensors only (no CPU path)")
-    p = [_arg(name, t.view(torch.uint8) if t.dtype is torch.float8_e4m3fn else t, torch.uint8, (*lead, n), dev)
+    p = [_arg(name, t.view(_U8) if t.dtype is torch.float8_e4m3fn else t, _U8, (*lead, n), dev)
          for name, t, n in (("k_codes", k_codes, 64), ("k_scales", k_scales, 8), ("v_codes", v_codes, 64),
                             ("v_scales", v_scales, 8))]
     table = None
@@ -387,7 +388,7 @@ def kv4_cache(k_codes, k_scales, v_codes, v_scales, page_table=None, page_tokens
     else:
         if page_table.dim() != 2:
             raise ValueError("page_table: i32 [batch][kv_capacity / page_tokens] expected")
-        table = _arg("page_table", page_table, torch.int32, tuple(page_table.shape), dev)
+        table = _arg("page_table", page_table, _I32, tuple(page_table.shape), dev)
         if lead[0] != n_pages or lead[2] != page_tokens:
             raise ValueError(f"pools of {n_pages} pages of {page_tokens} tokens expected, got {lead}")
         sizes = (page_table.shape[0], lead[1], page_table.shape[1] * page_tokens)
@@ -412,8 +413,8 @@ def qsa_kv4_append(dims, cache, k, v, cu_len, len_before, n_tok, workspace=None,
     _fits(dims, cache, dev)
     kp, k_ld = _rows_arg("k", k, n_tok, hkv, dev)
     vp, v_ld = _rows_arg("v", v, n_tok, hkv, dev)
-    rc = load().qsa_kv4_append(dims, cache, kp, k_ld, vp, v_ld, _arg("cu_len", cu_len, torch.int32, (batch + 1,), dev),
-                               _arg("len_before", len_before, torch.int32, (batch,), dev), n_tok,
+    rc = (_lib or load()).qsa_kv4_append(dims, cache, kp, k_ld, vp, v_ld, _arg("cu_len", cu_len, _I32, (batch + 1,), dev),
+                               _arg("len_before", len_before, _I32, (batch,), dev), n_tok,
                                _workspace_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_kv4_append", rc)
@@ -431,13 +432,13 @@ def qsa_sparse_attn_kv4(dims, cache, q, q_seq, q_pos, sel_idx, sel_cnt, n_q, out
     """qsa_sparse_attn_ex over a 4-bit cache (kv4_cache); needs no workspace but for its status."""
     dev, rows = _device_of(q), (n_q, dims.n_q_heads, 128)
     _fits(dims, cache, dev)
-    groups, i32 = n_q // group_q if group_q > 1 else n_q, torch.int32
-    args = qsa_attn_args(_arg("q", q, torch.bfloat16, rows, dev), None, None, _arg("q_seq", q_seq, i32, (n_q,), dev),
+    groups, i32 = n_q // group_q if group_q > 1 else n_q, _I32
+    args = qsa_attn_args(_arg("q", q, _BF16, rows, dev), None, None, _arg("q_seq", q_seq, i32, (n_q,), dev),
                          _arg("q_pos", q_pos, i32, (n_q,), dev),
                          _arg("sel_idx", sel_idx, i32, (groups, QSA_SEL_CAP), dev),
                          _arg("sel_cnt", sel_cnt, i32, (groups,), dev), n_q, group_q, None, 0, 0,
-                         _arg("out", out, torch.bfloat16, rows, dev))
-    rc = load().qsa_sparse_attn_kv4(dims, cache, args, _workspace_arg(workspace, dev), _stream_on(stream, dev))
+                         _arg("out", out, _BF16, rows, dev))
+    rc = (_lib or load()).qsa_sparse_attn_kv4(dims, cache, args, _workspace_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_sparse_attn_kv4", rc)
 
@@ -467,8 +468,8 @@ def qsa_pages_workspace_bytes(dims, page_tokens, n_pages):
 def _page_state(dims, pools, page_table, page_ref, dev):
     if pools.device is not None and pools.device != dev:
         raise ValueError(f"pools on cuda:{pools.device}, but the current device is cuda:{dev}")
-    return (_arg("page_table", page_table, torch.int32, (dims.batch, dims.kv_capacity // pools.page_tokens), dev),
-            _arg("page_ref", page_ref, torch.int32, (pools.n_pages,), dev))
+    return (_arg("page_table", page_table, _I32, (dims.batch, dims.kv_capacity // pools.page_tokens), dev),
+            _arg("page_ref", page_ref, _I32, (pools.n_pages,), dev))
 
 
 def _list_arg(name, t, n, dev):
@@ -477,16 +478,16 @@ def _list_arg(name, t, n, dev):
         return None
     if t is None or t.dim() != 1 or t.numel() < n:
         raise ValueError(f"{name}: {n} int32 values expected")
-    return _arg(name, t, torch.int32, t.shape, dev)
+    return _arg(name, t, _I32, t.shape, dev)
 
 
 def qsa_pages_update(dims, pools, page_table, page_ref, len_before, len_after, workspace, free_seq=None, n_free=0,
                      fork_src=None, fork_dst=None, n_fork=0, stream=None):
     """A scheduler's step on a paged cache (page_pools): free sequences, fork others, then make every
     page of positions [len_before, len_after) the sequence's own, copying what was shared."""
-    dev, i32, batch = _device_of(page_table), torch.int32, (dims.batch,)
+    dev, i32, batch = _device_of(page_table), _I32, (dims.batch,)
     table, ref = _page_state(dims, pools, page_table, page_ref, dev)
-    rc = load().qsa_pages_update(
+    rc = (_lib or load()).qsa_pages_update(
         dims, pools, table, ref, _list_arg("free_seq", free_seq, n_free, dev), n_free,
         _list_arg("fork_src", fork_src, n_fork, dev), _list_arg("fork_dst", fork_dst, n_fork, dev), n_fork,
         _arg("len_before", len_before, i32, batch, dev), _arg("len_after", len_after, i32, batch, dev),
@@ -499,7 +500,7 @@ def qsa_pages_compact(dims, pools, page_table, page_ref, n_live, workspace, stre
     """Move the live pages of every pool to the ids [0, n_live) (n_live: i32 [1], written)."""
     dev = _device_of(page_table)
     table, ref = _page_state(dims, pools, page_table, page_ref, dev)
-    rc = load().qsa_pages_compact(dims, pools, table, ref, _arg("n_live", n_live, torch.int32, (1,), dev),
+    rc = (_lib or load()).qsa_pages_compact(dims, pools, table, ref, _arg("n_live", n_live, _I32, (1,), dev),
                                   _workspace_arg(workspace, dev), workspace.nbytes, _stream_on(stream, dev))
     if rc:
         _check("qsa_pages_compact", rc)
