@@ -16,11 +16,12 @@
 // Work unit and splits: one CTA per (split, KV head, draft group), its rows the group's
 // query heads of that KV head (<= 32), tokens on the M side of mma.sync m16n8k16.  The
 // splits of a (group, KV head) form one thread-block cluster and read one another's partials
-// through shared memory, each finishing a share of the rows, so a call needs no scratch.  What differs from a bf16 gather is that
-// unpacking, not the copies, is the work (about 700 instructions per warp and 32 tokens,
-// 2.3 KB of each K and V), so operands never pass through shared memory unpacked and
-// warps do not wait for one another: each takes 32 tokens at a time through a ring of its
-// own (cp.async, four lanes per row of codes), and only the end is a block's.
+// through shared memory, each finishing a share of the rows, so a call needs no scratch.
+// What differs from a bf16 gather is that unpacking, not the copies, is the work (about 700
+// instructions per warp and 32 tokens, 2.3 KB of each K and V), so operands never pass
+// through shared memory unpacked and warps do not wait for one another: each takes 32 tokens
+// at a time through a ring of its own (cp.async, four lanes per row of codes), and only the
+// end is a block's.
 //
 // The contraction's order is free, so a lane takes 32 consecutive dims of its K rows (one
 // 16-byte shared load = all A fragments of a row, the query fragments use the same order),
@@ -30,10 +31,10 @@
 // than 2 (probabilities then reach 2^16 / 2, inside fp16), so accumulators are rescaled
 // in few steps.
 //
-// Measured: 1,024 queries of 2,052 tokens at 32 / 4 heads 271 us (ALU pipe two thirds busy: one
-// conversion per two values is what the format costs); a decode step of 16 x 64K contexts
-// 11.6 us (18.9 MB), of one 8K context with two drafts 9.8 us: round trips and one pass
-// through code that is not in the instruction cache yet.
+// Measured: 1,024 queries of 2,052 tokens at 32 / 4 heads 271 us (issue slots 68%, ALU pipe
+// 58% busy: one conversion per two values is what the format costs); a decode step of 16 x
+// 64K contexts 11.6 us (18.9 MB), of one 8K context with two drafts 9.8 us: round trips and
+// one pass through code that is not in the instruction cache yet.
 //
 // Masked places: absent tokens are zero-filled and their logits -inf.  A scale may be NaN
 // (the append writes that for values that are not finite): a draft's tail token that is
