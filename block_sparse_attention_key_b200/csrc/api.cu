@@ -558,8 +558,8 @@ static int check_page_sizes(const qsa_dims* d, int32_t page_tokens, int64_t n_pa
     if (page_tokens < 1 || page_tokens % d->block_size != 0 || d->kv_capacity % page_tokens != 0 || n_pages < 1 ||
         n_pages > (1ll << 31) - 1)
         return QSA_ERR_INVALID_ARG;
-    // scans run in strides of 8,192 pages, ranks over the whole table in 32 bits
-    return n_pages > (1ll << 30) || d->batch * (d->kv_capacity / page_tokens) > INT32_MAX ? QSA_ERR_UNSUPPORTED : QSA_OK;
+    // pages and table entries are counted in 32 bits, in strides of up to 8,192 past the last one
+    return n_pages > (1ll << 30) || d->batch * (d->kv_capacity / page_tokens) > (1ll << 30) ? QSA_ERR_UNSUPPORTED : QSA_OK;
 }
 
 static int check_pools(const qsa_dims* d, const qsa_page_pools* p, const int32_t* page_table, const int32_t* page_ref,
@@ -590,9 +590,9 @@ int qsa_pages_update(const qsa_dims* dims, const qsa_page_pools* pools, int32_t*
     int rc = check_dims(dims);
     if (rc != QSA_OK) return rc;
     if (n_free < 0 || n_fork < 0) return QSA_ERR_INVALID_ARG;
-    // entries of the named rows are counted in 32 bits
+    // so are the named sequences and the entries of their rows
     if (pools && pools->page_tokens > 0 &&
-        (int64_t)(n_free > n_fork ? n_free : n_fork) * (dims->kv_capacity / pools->page_tokens) > INT32_MAX)
+        (int64_t)(n_free > n_fork ? n_free : n_fork) * (dims->kv_capacity / pools->page_tokens) > (1ll << 30))
         return QSA_ERR_UNSUPPORTED;
     if ((n_free > 0 && !aligned16(free_seq)) || (n_fork > 0 && (!aligned16(fork_src) || !aligned16(fork_dst))) ||
         !aligned16(len_before) || !aligned16(len_after))

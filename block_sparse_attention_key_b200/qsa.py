@@ -9,8 +9,6 @@ There is no CPU fallback: if the library or a GPU is missing, calls raise.
 import ctypes
 import os
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libqsa.so")
 
@@ -201,6 +199,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
+    import torch
+
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -294,11 +294,29 @@ def qsa_forward(dims, *, q, k_cache, v_cache, idx_k, pooled, q_idx, w, len_befor
 
 # ---------------------------------------------------------------- checked arguments of the serving operators
 
-_BF16, _I32, _U8 = torch.bfloat16, torch.int32, torch.uint8
+# torch is imported with the first of these calls, as it is by _stream above
+_BF16 = _I32 = _U8 = _E4M3 = None
+
+
+def _bind_types():
+    global _BF16, _I32, _U8, _E4M3
+    import torch
+
+    _BF16, _I32, _U8, _E4M3 = torch.bfloat16, torch.int32, torch.uint8, torch.float8_e4m3fn
+
+
 # the calls behind torch.cuda.current_device() and current_stream(), without their wrappers' few
 # microseconds (a decode step's kernels take not many more); only used beside CUDA tensors
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
-_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _current_device():
+    global _current_device
+    from torch._C import _cuda_getDevice as _current_device
+    return _current_device()
+
+
+def _current_stream(dev):
+    global _current_stream
+    from torch._C import _cuda_getCurrentRawStream as _current_stream
+    return _current_stream(dev)
 
 
 def _stream_on(stream, dev):
@@ -309,6 +327,8 @@ def _stream_on(stream, dev):
 
 def _device_of(t):
     """Device index of a call's first tensor.  Launches go to the current device, so it has to be that."""
+    if _BF16 is None:
+        _bind_types()
     dev = t.get_device()
     if dev < 0:
         raise ValueError("libqsa takes CUDA tensors only (no CPU path)")
@@ -376,10 +396,12 @@ def kv4_cache(k_codes, k_scales, v_codes, v_scales, page_table=None, page_tokens
     lead = tuple(k_codes.shape[:-1])
     if len(lead) != 3:
         raise ValueError("codes: [batch or pages][n_kv_heads][tokens][64] expected")
+    if _U8 is None:
+        _bind_types()
     dev = k_codes.get_device()
     if dev < 0:
         raise ValueError("libqsa takes CUDA tensors only (no CPU path)")
-    p = [_arg(name, t.view(_U8) if t.dtype is torch.float8_e4m3fn else t, _U8, (*lead, n), dev)
+    p = [_arg(name, t.view(_U8) if t.dtype is _E4M3 else t, _U8, (*lead, n), dev)
          for name, t, n in (("k_codes", k_codes, 64), ("k_scales", k_scales, 8), ("v_codes", v_codes, 64),
                             ("v_scales", v_scales, 8))]
     table = None
@@ -413,9 +435,9 @@ def qsa_kv4_append(dims, cache, k, v, cu_len, len_before, n_tok, workspace=None,
     _fits(dims, cache, dev)
     kp, k_ld = _rows_arg("k", k, n_tok, hkv, dev)
     vp, v_ld = _rows_arg("v", v, n_tok, hkv, dev)
-    rc = (_lib or load()).qsa_kv4_append(dims, cache, kp, k_ld, vp, v_ld, _arg("cu_len", cu_len, _I32, (batch + 1,), dev),
-                               _arg("len_before", len_before, _I32, (batch,), dev), n_tok,
-                               _workspace_arg(workspace, dev), _stream_on(stream, dev))
+    rc = (_lib or load()).qsa_kv4_append(
+        dims, cache, kp, k_ld, vp, v_ld, _arg("cu_len", cu_len, _I32, (batch + 1,), dev),
+        _arg("len_before", len_before, _I32, (batch,), dev), n_tok, _workspace_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_kv4_append", rc)
 
@@ -450,6 +472,8 @@ def page_pools(pools, page_tokens, n_pages):
     type (K and V, or codes and scales, of every layer).  It keeps them alive; make it once."""
     if len(pools) > QSA_MAX_POOLS:
         raise ValueError(f"at most {QSA_MAX_POOLS} pools")
+    if n_pages < 1:
+        raise ValueError("at least one page expected")
     p = qsa_page_pools(len(pools), page_tokens, n_pages)
     for i, t in enumerate(pools):
         if t.shape[0] != n_pages:
@@ -472,6 +496,13 @@ def _page_state(dims, pools, page_table, page_ref, dev):
             _arg("page_ref", page_ref, _I32, (pools.n_pages,), dev))
 
 
+def _scratch_arg(workspace, dev):
+    """Pointer and bytes of a workspace that the call needs."""
+    if workspace is None:
+        raise ValueError("workspace: a tensor of qsa_pages_workspace_bytes expected")
+    return _workspace_arg(workspace, dev), workspace.nbytes
+
+
 def _list_arg(name, t, n, dev):
     """Pointer of the first n of a list of sequences."""
     if n <= 0:
@@ -491,7 +522,7 @@ def qsa_pages_update(dims, pools, page_table, page_ref, len_before, len_after, w
         dims, pools, table, ref, _list_arg("free_seq", free_seq, n_free, dev), n_free,
         _list_arg("fork_src", fork_src, n_fork, dev), _list_arg("fork_dst", fork_dst, n_fork, dev), n_fork,
         _arg("len_before", len_before, i32, batch, dev), _arg("len_after", len_after, i32, batch, dev),
-        _workspace_arg(workspace, dev), workspace.nbytes, _stream_on(stream, dev))
+        *_scratch_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_pages_update", rc)
 
@@ -501,7 +532,7 @@ def qsa_pages_compact(dims, pools, page_table, page_ref, n_live, workspace, stre
     dev = _device_of(page_table)
     table, ref = _page_state(dims, pools, page_table, page_ref, dev)
     rc = (_lib or load()).qsa_pages_compact(dims, pools, table, ref, _arg("n_live", n_live, _I32, (1,), dev),
-                                  _workspace_arg(workspace, dev), workspace.nbytes, _stream_on(stream, dev))
+                                  *_scratch_arg(workspace, dev), _stream_on(stream, dev))
     if rc:
         _check("qsa_pages_compact", rc)
 

@@ -315,8 +315,7 @@ int qsa_forward(const qsa_dims* dims, const qsa_forward_args* args, void* worksp
  * bf16 caches with 64 or 8 bytes in the place of the 128 values: [batch][n_kv_heads]
  * [kv_capacity][64 | 8], or with page_table != NULL pools [n_pages][n_kv_heads]
  * [page_tokens][64 | 8] (see qsa_sparse_attn_ex), fewer than 2^32 - 1 token rows in all.
- * All pointers 16-byte aligned.  The
- * indexer's keys and the pooled cache stay as they are. */
+ * All pointers 16-byte aligned.  The indexer's keys and the pooled cache stay as they are. */
 typedef struct qsa_kv4_cache {
     void* k_codes;              /* u8 */
     void* k_scales;             /* e4m3 */
@@ -362,7 +361,9 @@ int qsa_attn_kv4_plan(const qsa_dims* dims, int32_t n_q, int32_t group_q, qsa_at
  * two calls below keep them consistent.  Sequences forked from one another share pages
  * until one of them appends.  One table serves every layer and array that is paged alike:
  * `pools` names them all (K and V, or codes and scales, of each layer), page p of pool i
- * being bytes [p * page_bytes[i], (p + 1) * page_bytes[i]) (page_bytes a multiple of 16). */
+ * being bytes [p * page_bytes[i], (p + 1) * page_bytes[i]) (page_bytes a multiple of 16, at
+ * most 2^31).  At most 2^30 pages, table entries, and entries of the sequences that one call
+ * frees or forks. */
 #define QSA_MAX_POOLS 128
 
 typedef struct qsa_page_pools {

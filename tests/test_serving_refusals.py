@@ -1,6 +1,7 @@
 """Argument checks of the serving operators: host only, nothing is launched."""
 
 import ctypes
+import os
 
 import pytest
 import torch
@@ -243,6 +244,13 @@ def test_pages_refusals(qsa):
     for kw in (dict(p=pools(n_pages=(1 << 30) + 1)), dict(p=pools(size=(1 << 31) + 16)),
                dict(dims=_dims(qsa, batch=65535, kv_capacity=1 << 20))):
         assert update(**kw) == compact(**kw) == qsa.QSA_ERR_UNSUPPORTED, kw
+    # counters run up to a stride past the last entry: 2^30 entries are the most
+    wide = _dims(qsa, batch=32, kv_capacity=(1 << 30) // 32 * 16)
+    assert update(dims=wide, n=0) == compact(dims=wide, n=0) == qsa.QSA_ERR_WORKSPACE_TOO_SMALL
+    wider = _dims(qsa, batch=33, kv_capacity=(1 << 30) // 32 * 16)
+    assert update(dims=wider) == compact(dims=wider) == qsa.QSA_ERR_UNSUPPORTED
+    entries = d.kv_capacity // 16
+    assert update(n_free=(1 << 30) // entries + 1) == update(n_fork=(1 << 30) // entries + 1) == qsa.QSA_ERR_UNSUPPORTED
     for bad in ((d, 16, 0), (d, 5, 10), (_dims(qsa, top_k=0), 16, 10), (_dims(qsa, batch=65535, kv_capacity=1 << 20), 16, 10)):
         assert qsa.qsa_pages_workspace_bytes(*bad) == 0
 
@@ -264,5 +272,19 @@ def test_pages_binding_checks(qsa, device0):
                                  fork_src=a["src"], fork_dst=a["dst"], n_fork=a["n_fork"])
     with pytest.raises(ValueError, match="n_live"):
         qsa.qsa_pages_compact(d, p, table, ref, _on(2), ws)
+    with pytest.raises(ValueError, match="workspace"):
+        qsa.qsa_pages_compact(d, p, table, ref, _on(1), None)
+    with pytest.raises(ValueError, match="workspace"):
+        qsa.qsa_pages_update(d, p, table, ref, n4, n4, None)
+    with pytest.raises(ValueError, match="one page"):
+        qsa.page_pools([_on(0, 16)], 16, 0)
     with pytest.raises(ValueError, match="current device"):
         qsa.qsa_pages_compact(d, p, table, _on(7, dev=1), _on(1), ws)
+
+
+def test_package_import_leaves_torch_alone():
+    """The binding's calls by pointer need no torch; it is imported with the first call that takes tensors."""
+    import subprocess
+    import sys
+    code = "import sys, block_sparse_attention_key_b200; sys.exit('torch' in sys.modules)"
+    assert subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__)))).returncode == 0
