@@ -34,7 +34,8 @@
  *   make the kernels skip the offending work and set a bit in the workspace's
  *   device status word (QSA_DEV_*), read with qsa_read_device_status().  No kernel
  *   traps, asserts or waits without bound.
- * - Outputs never alias inputs; `pooled` is the only in-out tensor.
+ * - Outputs never alias inputs; the in-out tensors are `pooled` and, of the calls that
+ *   keep them, 4-bit caches, page tables, page counts and page pools.
  *
  * Block size and budget: the published setting is 4-token blocks and 512 blocks
  * per query; dims.block_size may be any power of two up to 16 (1 = per-token
@@ -375,7 +376,8 @@ typedef struct qsa_page_pools {
 } qsa_page_pools;
 
 /* Workspace bytes of the two calls (0 on invalid arguments); initialise it with
- * qsa_workspace_init.  A larger workspace of another call serves as well. */
+ * qsa_workspace_init.  A larger workspace of another call serves as well, but calls whose
+ * executions may overlap on the GPU need one each and work on different tables. */
 size_t qsa_pages_workspace_bytes(const qsa_dims* dims, int32_t page_tokens, int64_t n_pages);
 
 /* A scheduler's step, before the appends of the next model step.  In this order:
