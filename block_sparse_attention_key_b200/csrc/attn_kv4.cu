@@ -28,10 +28,10 @@
 // and 16 consecutive dims of its V tokens (8 bytes and one scale each); V pairs are two
 // tokens of one dim: their nibbles are interleaved with bit selects before the conversion
 // (4 logic operations per 16 values).  The running maximum moves when it grew by more
-// than 2 (probabilities then reach 2^16 / 2, inside fp16), so accumulators are rescaled
-// in few steps.
+// than 2 (probabilities then reach 2^16 / 2, inside fp16), so accumulators are rescaled,
+// and lanes compare their maxima at all, in few steps.
 //
-// Measured: 1,024 queries of 2,052 tokens at 32 / 4 heads 271 us (issue slots 68%, ALU pipe
+// Measured: 1,024 queries of 2,052 tokens at 32 / 4 heads 261 us (issue slots 68%, ALU pipe
 // 58% busy: one conversion per two values is what the format costs); a decode step of 16 x
 // 64K contexts 11.6 us (18.9 MB), of one 8K context with two drafts 9.8 us: round trips and
 // one pass through code that is not in the instruction cache yet.
@@ -186,10 +186,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 
 }  // namespace
 
+// CTAs per SM that the registers have to leave room for: 128 a thread with one row tile, 168 and
+// 255 with two and four.  One CTA fewer of four warps costs more than the spare registers give
+// (2,368 lists of 16 rows: 259 us with two of 193, 222 us with three of 168).
+constexpr int ctas_per_sm4(int nt, int warps) { return nt == 1 ? 16 / warps : warps == 4 ? (nt == 2 ? 3 : 2) : 1; }
+
 // NT = 8-row column tiles of the MMA's N side (rows = drafts x G <= 8 * NT); KW = warps;
 // D = tiles in flight per warp.
 template <int NT, int KW, int D>
-__global__ void __launch_bounds__(32 * KW)
+__global__ void __launch_bounds__(32 * KW, ctas_per_sm4(NT, KW))
 k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_codes,
                   const uint8_t* __restrict__ k_scales, const uint8_t* __restrict__ v_codes,
                   const uint8_t* __restrict__ v_scales, const int32_t* __restrict__ q_seq,
@@ -417,9 +422,10 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2], up[NT][2];   // up: kProbShift - m, of the maximum 0 while there is none
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
+    for (int nt = 0; nt < NT; ++nt)
+        m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f, up[nt][0] = up[nt][1] = kProbShift;
     // token (of 16) of MMA row r, in either half of a tile: r / 2 for even r, 4 + (r / 2 ^ 1) for
     // odd r, + 8 for rows 8 and up.  Two neighbouring rows lie in different halves of 128 bytes
     // (K's reads), the even rows are tokens 0 to 3 (V's reads)
@@ -476,12 +482,6 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
             }
         }
         // ---- softmax: element e of half h: token 16 h + tk (+8 for e >= 2), row 8nt + 2c4 + (e & 1) ----
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[h][nt][e] *= rsc[nt][e & 1];
         if (masked) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -499,21 +499,26 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float x = fmaxf(fmaxf(sc[0][nt][j], sc[0][nt][j + 2]), fmaxf(sc[1][nt][j], sc[1][nt][j + 2]));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                mx[nt][j] = x;
-                grow = grow || x > m[nt][j] + kGrow4;
+                // of the lane's tokens; of all 32 only where some lane's maximum grew
+                mx[nt][j] = fmaxf(fmaxf(sc[0][nt][j], sc[0][nt][j + 2]), fmaxf(sc[1][nt][j], sc[1][nt][j + 2])) *
+                            rsc[nt][j];
+                grow = grow || mx[nt][j] > m[nt][j] + kGrow4;
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const bool g_ = mx[nt][j] > m[nt][j] + kGrow4;
-                    const float f = g_ ? exp2_approx(m[nt][j] - mx[nt][j]) : 1.0f;
-                    if (g_) m[nt][j] = mx[nt][j];
+                    float x = mx[nt][j];
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    const bool g_ = x > m[nt][j] + kGrow4;
+                    const float f = g_ ? exp2_approx(m[nt][j] - x) : 1.0f;
+                    if (g_) {
+                        m[nt][j] = x;
+                        up[nt][j] = kProbShift - x;
+                    }
                     l[nt][j] *= f;
 #pragma unroll
                     for (int mt = 0; mt < 8; ++mt) {
@@ -525,12 +530,11 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         uint32_t pb[2][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float u0 = kProbShift - (m[nt][0] == -INFINITY ? 0.f : m[nt][0]);
-            const float u1 = kProbShift - (m[nt][1] == -INFINITY ? 0.f : m[nt][1]);
+            const float r0 = rsc[nt][0], r1 = rsc[nt][1], u0 = up[nt][0], u1 = up[nt][1];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float p0 = exp2_approx(sc[h][nt][0] + u0), p1 = exp2_approx(sc[h][nt][1] + u1);
-                const float p2 = exp2_approx(sc[h][nt][2] + u0), p3 = exp2_approx(sc[h][nt][3] + u1);
+                const float p0 = exp2_approx(fmaf(sc[h][nt][0], r0, u0)), p1 = exp2_approx(fmaf(sc[h][nt][1], r1, u1));
+                const float p2 = exp2_approx(fmaf(sc[h][nt][2], r0, u0)), p3 = exp2_approx(fmaf(sc[h][nt][3], r1, u1));
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
                 pb[h][nt][0] = movm_t(pack_f16(p0, p1));  // MMA rows 0-7 -> B operand (k = token, n = row)
@@ -730,12 +734,13 @@ int nt_for(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 // one CTA per SM (or a cluster per list), as many warps as its registers allow.  More: smaller
 // CTAs, several per SM, whose starts and ends overlap and whose last wave is shorter.  Lists of
 // 2,052 tokens, us:
-//   <= 8 rows, 16 / 8 / 4 / 2 warps: 148 lists 15.6 / 17.2 / 23.1 / 40, 296 lists 29.4 / 25.2 /
-//   28.5 / 41, 400 lists 42.1 / 37.5 / 36.2 / 50, 4,096 lists 371 / 292 / 271 / 268
-//   <= 16 rows, 8 / 4 / 2 warps: 148 lists 23.0 / 30.2 / 45.2, 200 lists 43.1 / 36.4 / 45.9,
-//   2,368 lists 333 / 232 / 233
-//   <= 32 rows, 8 / 4 / 2 warps: 148 lists 33.3 / 42.0 / 72.5, 200 lists 62.4 / 53.8 / 74.5,
-//   400 lists 93 / 100 / 98, 2,368 lists 488 / 409 / 387
+//   <= 8 rows, 8 / 4 / 2 warps: 148 lists 16.8 / 21.4 / 39.5, 296 lists 24.7 / 27.5 / 40.4,
+//   400 lists 36.4 / 35.1 / 49.5, 4,096 lists 283 / 261 / 255; 16 warps (measured with a loop
+//   about 3% slower): 15.6, 29.4, 42.1 and 371
+//   <= 16 rows, 8 / 4 / 2 warps: 148 lists 20.6 / 28.6 / 43.2, 149 lists 37.3 / 35.4 / 43.5,
+//   400 lists 56.6 / 45.1 / 58.0, 2,368 lists 294 / 222 / 224
+//   <= 32 rows, 8 / 4 / 2 warps: 148 lists 33.3 / 41.9 / 72.5, 149 lists 59.9 / 52.7 / 73.3,
+//   400 lists 92 / 90 / 97, 2,368 lists 483 / 405 / 384
 int tier4(int64_t lists) { return lists <= 148 ? 0 : lists <= 296 ? 1 : 2; }
 
 struct Shape {
