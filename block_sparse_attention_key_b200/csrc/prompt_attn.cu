@@ -34,7 +34,9 @@
 //   warps 2-3    V guard: in the key tiles that some row masks, values of V that are
 //                not finite become 0 before the MMA reads them (0 x inf would put a NaN
 //                into rows that must not see the token), and the first token holding
-//                one is kept per dim; the epilogue gives it back to the rows behind it;
+//                one is kept per dim; the epilogue gives it back to the rows behind it.
+//                Each guard warp has one 64-dim half of the tile with that half's marks
+//                and flag to itself, so the two never wait for each other;
 //   warps 4-11   softmax, four warps per query tile, one row per thread: S from TMEM,
 //                exponentials, P back to TMEM in two parts (the MMA starts on the first);
 //                at the end O / l to global memory, 32 bytes per store.
@@ -93,7 +95,7 @@ struct __align__(1024) PromptSmem {
     uint64_t item_full[kItems], item_empty[kItems], next_full, mma_done;
     uint64_t tile_done[2];                         // a tile's epilogue is over
     uint32_t tmem_base;
-    int error, any_bad;
+    int error, any_bad[2];                         // any_bad: a mark of `bad` is set, per dim half
 };
 
 __device__ __forceinline__ float exp2_approx(float x)
@@ -224,7 +226,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     }
     if (warp == 2 && lane == 0) {
         S.error = 0;
-        S.any_bad = 0;
+        S.any_bad[0] = S.any_bad[1] = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&S.q_full[i], 1);
             mbar_init(&S.q_empty[i], 1);
@@ -446,8 +448,8 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             while (!mbar_try_wait(&S.mma_done, 0) && now_ns() - t < kWaitNs) {
             }
         } else {
-            // ---------------- V guard: 64 threads over the 32 KiB of each masked V tile ----------------
-            const int gt = (warp - 2) * 32 + lane;
+            // ---------------- V guard: a warp per 64-dim half (16 KiB) of each masked V tile ----------------
+            const int half = warp - 2;
             int k_ring = 0, n_mask = 0, n_done_b = 0;
             bool had_b = false;
             Item it;
@@ -459,28 +461,31 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 if (ok && had_b) ok = wait_phase(&S.tile_done[1], n_done_b++ & 1, err, status);
                 if (!ok) break;
                 had_b = t.n_b > 0;
-                if (*(volatile int*)&S.any_bad) {
-                    asm volatile("bar.sync 1, 64;\n" ::: "memory");
-                    for (int k = gt; k < 3 * kHeadDim; k += 64) (&S.bad[0][0])[k] = INT_MAX;
-                    S.any_bad = 0;
-                    asm volatile("bar.sync 1, 64;\n" ::: "memory");
+                // the flag is this warp's own: every lane has read it before one clears it, and the
+                // marks are cleared before the warp sets the next
+                const int marked = *(volatile int*)&S.any_bad[half];
+                __syncwarp();
+                if (marked) {
+                    for (int k = lane; k < 3 * 64; k += 32) S.bad[k >> 6][half * 64 + (k & 63)] = INT_MAX;
+                    S.any_bad[half] = 0;
+                    __syncwarp();
                 }
                 for (int j = t.j_mask; j < t.n_kv && ok; ++j) {
                     const int g = n_mask++;
                     if (!(ok = wait_phase(&S.v_full[g % kGuards], (g / kGuards) & 1, err, status))) break;
-                    uint4* tile = reinterpret_cast<uint4*>(S.kv[(k_ring + 2 * j + 1) % kRing][0]);
+                    uint4* tile = reinterpret_cast<uint4*>(S.kv[(k_ring + 2 * j + 1) % kRing][half]);
                     bool wrote = false;
 #pragma unroll 4
-                    for (int c = gt; c < (int)(kTileBytes / 16); c += 64) {
+                    for (int c = lane; c < (int)(kTileBytes / 32); c += 32) {
                         uint4 v = tile[c];
                         uint32_t w[4] = {v.x, v.y, v.z, v.w};
                         uint32_t hit = 0;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) hit |= ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
                         if (hit == 0) continue;
-                        // chunk c: half c >> 10, token row (c >> 3) & 127, swizzled 16-byte chunk c & 7
-                        const int row = (c >> 3) & 127, tok = j * kKeys + row;
-                        const int dim0 = (c >> 10) * 64 + (((c & 7) ^ (row & 7)) << 3);
+                        // chunk c: token row c >> 3, swizzled 16-byte chunk c & 7
+                        const int row = c >> 3, tok = j * kKeys + row;
+                        const int dim0 = half * 64 + (((c & 7) ^ (row & 7)) << 3);
                         for (int e = 0; e < 8; ++e) {
                             const uint32_t b = (w[e >> 1] >> ((e & 1) * 16)) & 0xFFFFu;
                             if ((b & 0x7F80u) != 0x7F80u) continue;
@@ -491,7 +496,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                         tile[c] = make_uint4(w[0], w[1], w[2], w[3]);
                         wrote = true;
                     }
-                    if (wrote) S.any_bad = 1;
+                    if (wrote) S.any_bad[half] = 1;
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&S.v_clean[g % kGuards]);
@@ -614,7 +619,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 tc_fence_after();
                 const float l = __uint_as_float((unsigned)l2) + __uint_as_float((unsigned)(l2 >> 32));
                 const float inv = 1.0f / l;
-                const bool bad = *(volatile int*)&S.any_bad != 0;
+                const bool bad = (*(volatile int*)&S.any_bad[0] | *(volatile int*)&S.any_bad[1]) != 0;
                 const bool live = row < ta * G && tok < it.len;
                 char* dst = reinterpret_cast<char*>(
                     out + ((int64_t)(it.tok0 + tok) * n_q_heads + it.head * G + row_head) * kHeadDim);

@@ -261,3 +261,37 @@ def test_equals_the_sparse_layer_below_its_budget():
     # both within the tolerance above of the same value
     tol = 2 * (2.0 ** -8 * out.double().abs() + (2.0 ** -8 + 2.0 ** -10) * mag)
     assert ((sparse.double() - out.double()).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("hq,hkv,n_seq,longest", [(16, 16, 400, 160), (16, 2, 30, 700), (4, 4, 300, 300)])
+def test_values_that_are_not_finite_in_many_items(hq, hkv, n_seq, longest):
+    """Dozens of items per CTA, in most of them V values that are not finite under the mask: the marks
+    of one item are gone before the next, in both halves of the dims, and every launch gives the same bits."""
+    g = torch.Generator().manual_seed(hq + n_seq)
+    lens = torch.randint(1, longest + 1, (n_seq,), generator=g).tolist()
+    cu, n = _cu(lens), sum(lens)
+    q, k, v = _inputs(n, hq, hkv, 17)
+    bad = torch.rand((n, hkv, 128), generator=torch.Generator(device="cuda").manual_seed(18), device="cuda")
+    kinds = ((math.inf, (0.0, 2e-4)), (-math.inf, (2e-4, 4e-4)), (math.nan, (4e-4, 5e-4)))
+    v0, v1 = v.clone(), v.clone()
+    seen = []
+    for value, (lo, hi) in kinds:
+        here = (bad >= lo) & (bad < hi)
+        v0[here], v1[here] = 0.0, value
+        past = torch.cat([here[a:b].cumsum(0) > 0 for a, b in zip(cu[:-1], cu[1:])])
+        seen.append(past.repeat_interleave(hq // hkv, 1))
+    clean, flags = _run(q, k, v0, cu)
+    assert flags == 0
+    _check(clean, q, k, v0, cu)
+    up, dn, nan = seen
+    nan = nan | (up & dn)
+    want = clean.masked_fill(up, math.inf).masked_fill(dn, -math.inf)
+    dims = qsa.make_dims(n_seq, hq, hkv, 8192)
+    cu_t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    ws, out = gu.new_workspace(256), torch.empty_like(clean)
+    for _ in range(40):
+        out.fill_(77.0)
+        qsa.qsa_prompt_attn(dims, q, k, v1, cu_t, n, out, ws)
+        assert qsa.qsa_read_device_status(ws) == 0
+        assert torch.equal(out.isnan(), nan)
+        assert torch.equal(out[~nan], want[~nan])
