@@ -304,7 +304,8 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                 ++asked;
                 if (it.len > 0) {
                     const int slot = n_item % kItems;
-                    if (n_item >= kItems && !wait_phase(&S.item_empty[slot], ((n_item / kItems) - 1) & 1, err, status)) break;
+                    if (n_item >= kItems && !(ok = wait_phase(&S.item_empty[slot], ((n_item / kItems) - 1) & 1, err, status)))
+                        break;
                     if (lane == 0) {
                         S.item[slot] = it;
                         mbar_arrive(&S.item_full[slot]);
@@ -351,12 +352,6 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                         S.item[slot].len = 0;
                         mbar_arrive(&S.item_full[slot]);
                     }
-            } else if (lane == 0) {
-                // drain: what is on its way into shared memory must land before the CTA exits
-                // (1 ms, some thousand times a tile's latency)
-                const uint64_t t = now_ns();
-                while (now_ns() - t < 1000000) {
-                }
             }
         } else if (warp == 1) {
             // ---------------- MMA ----------------
@@ -669,6 +664,14 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, kTmemColsPrompt);
+    }
+    if (tid == 0 && *err) {
+        // drain after any role has given up: what is on its way into shared memory (tiles, the
+        // answer about the next CTA) must land before the CTA ends (1 ms, some thousand times a
+        // tile's latency)
+        const uint64_t t = now_ns();
+        while (now_ns() - t < 1000000) {
+        }
     }
 }
 
