@@ -142,7 +142,8 @@ k_pages_update(int32_t* table, int32_t* ref, int batch, int table_ld, int page_t
             return atomicExch(table + (int64_t)s * table_ld + c, -1);
         },
         [&](uint32_t, uint32_t, int e) {
-            if (e >= 0 && e < n_pages) atomicSub(ref + e, 1);
+            if (e >= n_pages) set_status(status, QSA_DEV_BAD_PAGE);
+            else if (e >= 0) atomicSub(ref + e, 1);
         });
 
     // ---- fork: a target counts once (its first fork), holds nothing and is nobody's source ----
@@ -228,8 +229,11 @@ k_pages_update(int32_t* table, int32_t* ref, int batch, int table_ld, int page_t
                 const int i = s_lo[t] + (c - s_at[t]);
                 place = (uint32_t)((int64_t)(s0 + t) * table_ld + i);
                 e = __ldcg(table + place);
-                if (e < 0 || e >= n_pages) e = -1, needs = 1;
-                else if (__ldcg(ref + e) > 1) needs = (int64_t)i * page_tokens < s_lb[t] ? 2 : 1;
+                if (e < 0 || e >= n_pages) {
+                    // tokens that should be there are lost; a place that holds none yet just gets a page
+                    if (e >= 0 && (int64_t)i * page_tokens < s_lb[t]) set_status(status, QSA_DEV_BAD_PAGE);
+                    e = -1, needs = 1;
+                } else if (__ldcg(ref + e) > 1) needs = (int64_t)i * page_tokens < s_lb[t] ? 2 : 1;
             }
             int more;
             const int rank = wanted + block_scan(needs != 0, &more);

@@ -397,7 +397,8 @@ size_t qsa_pages_workspace_bytes(const qsa_dims* dims, int32_t page_tokens, int6
  * the caller.  Device status: QSA_DEV_BAD_SEQ (a free or fork that names no sequence, or
  * a fork that breaks the rules above: skipped), QSA_DEV_BAD_LEN (lengths outside
  * [0, kv_capacity] or decreasing: nothing reserved), QSA_DEV_BAD_PAGE (an entry past
- * n_pages, taken for -1, or not enough free pages: the places left over keep their
+ * n_pages, taken for -1, in a row that is freed or forked or where tokens below
+ * len_before should be; or not enough free pages: the places left over keep their
  * entries, and the call may be repeated with n_free = n_fork = 0 once there are some). */
 int qsa_pages_update(const qsa_dims* dims, const qsa_page_pools* pools, int32_t* page_table, int32_t* page_ref,
                      const int32_t* free_seq, int32_t n_free, const int32_t* fork_src, const int32_t* fork_dst,

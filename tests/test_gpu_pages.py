@@ -204,6 +204,46 @@ def test_bad_names_and_lengths_are_reported_and_skipped():
     p.same(p.data)
 
 
+def test_entries_past_the_pool_are_reported_where_tokens_should_be():
+    """Freed, forked, or appended to behind earlier tokens: taken for none and reported."""
+    none = [0] * 4
+
+    def step(p, before, after, free=(), forks=(), want=BAD_PAGE):
+        data = [d.clone() for d in p.data]
+        flags, moves = p.m.update(free, forks, before, after)
+        assert flags == 0 and not moves                  # the model has -1 for an entry that the call looks at
+        qsa.qsa_pages_update(p.dims, p.pools, p.table, p.ref, _i32(before), _i32(after), p.ws,
+                             free_seq=_i32(free), n_free=len(free), fork_src=_i32([a for a, _ in forks]),
+                             fork_dst=_i32([b for _, b in forks]), n_fork=len(forks))
+        assert qsa.qsa_read_device_status(p.ws) == want
+        p.same(data)
+
+    for entry in (20, 1 << 20, (1 << 31) - 1):
+        p = Pool(4, 4, 20, 4)
+        assert p.update([], [], none, [10, 7, 0, 0]) == 0
+        p.table[1, 1] = p.m.table[1][1] = entry          # its page stays counted: nothing names it any more
+        step(p, [10, 7, 0, 0], [11, 7, 0, 0], want=0)    # nobody looks at it
+        p.m.table[1][1] = -1
+        step(p, [11, 7, 0, 0], [11, 9, 0, 0])            # tokens 4 to 6 should be in the place of token 7
+        p.table[0, 2], p.m.table[0][2] = entry, -1
+        p.m.table[2] = list(p.m.table[0])
+        for e in p.m.table[2]:
+            if e >= 0:
+                p.m.ref[e] += 1
+        data = [d.clone() for d in p.data]
+        qsa.qsa_pages_update(p.dims, p.pools, p.table, p.ref, _i32(none), _i32(none), p.ws, fork_src=_i32([0]),
+                             fork_dst=_i32([2]), n_fork=1)
+        assert qsa.qsa_read_device_status(p.ws) == BAD_PAGE
+        assert p.table[0, 2] == entry                    # the source keeps its entry
+        p.table[0, 2] = -1
+        p.same(data)
+        p.table[2, 3] = entry
+        step(p, none, none, free=[2])
+        step(p, none, none, free=[2], want=0)            # emptied: not reported twice
+        p.table[0, 3] = entry
+        step(p, [12, 0, 0, 0], [13, 0, 0, 0], want=0)    # a place without tokens just gets a page
+
+
 def test_a_rolled_back_sequence_leaves_its_siblings_pages_alone():
     """Speculation went past a page and is taken back into a shared one: the append copies it."""
     p = Pool(2, 4, 12, 4)
