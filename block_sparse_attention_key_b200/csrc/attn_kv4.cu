@@ -105,6 +105,19 @@ __device__ __forceinline__ float exp2_approx(float x)
     return y;
 }
 
+// two fp32 in one register pair, and (s + n) * r + kProbShift of both: two instructions
+__device__ __forceinline__ unsigned long long pair(float lo, float hi)
+{
+    return ((unsigned long long)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+}
+__device__ __forceinline__ float2 shifted2(unsigned long long s, unsigned long long n, unsigned long long r)
+{
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(s), "l"(n));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(d), "l"(r), "l"(pair(kProbShift, kProbShift)));
+    return make_float2(__uint_as_float((unsigned)d), __uint_as_float((unsigned)(d >> 32)));
+}
+
 __device__ __forceinline__ uint4 lds128(uint32_t a)
 {
     uint4 v;
@@ -422,10 +435,13 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) o[mt][nt][0] = o[mt][nt][1] = o[mt][nt][2] = o[mt][nt][3] = 0.f;
-    float m[NT][2], l[NT][2], up[NT][2];   // up: kProbShift - m, of the maximum 0 while there is none
+    // running maxima before the logit scale, so that an exponent is the scaled difference of two
+    // products: exactly 0 at the maximum however large the logits are.  neg: -m, of the maximum 0
+    // while there is none
+    float m[NT][2], l[NT][2], neg[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
-        m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f, up[nt][0] = up[nt][1] = kProbShift;
+        m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f, neg[nt][0] = neg[nt][1] = 0.f;
     // token (of 16) of MMA row r, in either half of a tile: r / 2 for even r, 4 + (r / 2 ^ 1) for
     // odd r, + 8 for rows 8 and up.  Two neighbouring rows lie in different halves of 128 bytes
     // (K's reads), the even rows are tokens 0 to 3 (V's reads)
@@ -500,9 +516,8 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 // of the lane's tokens; of all 32 only where some lane's maximum grew
-                mx[nt][j] = fmaxf(fmaxf(sc[0][nt][j], sc[0][nt][j + 2]), fmaxf(sc[1][nt][j], sc[1][nt][j + 2])) *
-                            rsc[nt][j];
-                grow = grow || mx[nt][j] > m[nt][j] + kGrow4;
+                mx[nt][j] = fmaxf(fmaxf(sc[0][nt][j], sc[0][nt][j + 2]), fmaxf(sc[1][nt][j], sc[1][nt][j + 2]));
+                grow = grow || (mx[nt][j] - m[nt][j]) * rsc[nt][j] > kGrow4;
             }
         if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
@@ -513,11 +528,11 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    const bool g_ = x > m[nt][j] + kGrow4;
-                    const float f = g_ ? exp2_approx(m[nt][j] - x) : 1.0f;
+                    const bool g_ = (x - m[nt][j]) * rsc[nt][j] > kGrow4;
+                    const float f = g_ ? exp2_approx((m[nt][j] - x) * rsc[nt][j]) : 1.0f;
                     if (g_) {
                         m[nt][j] = x;
-                        up[nt][j] = kProbShift - x;
+                        neg[nt][j] = -x;
                     }
                     l[nt][j] *= f;
 #pragma unroll
@@ -530,11 +545,13 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         uint32_t pb[2][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float r0 = rsc[nt][0], r1 = rsc[nt][1], u0 = up[nt][0], u1 = up[nt][1];
+            const unsigned long long r2 = pair(rsc[nt][0], rsc[nt][1]), n2 = pair(neg[nt][0], neg[nt][1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float p0 = exp2_approx(fmaf(sc[h][nt][0], r0, u0)), p1 = exp2_approx(fmaf(sc[h][nt][1], r1, u1));
-                const float p2 = exp2_approx(fmaf(sc[h][nt][2], r0, u0)), p3 = exp2_approx(fmaf(sc[h][nt][3], r1, u1));
+                const float2 a = shifted2(pair(sc[h][nt][0], sc[h][nt][1]), n2, r2);
+                const float2 b = shifted2(pair(sc[h][nt][2], sc[h][nt][3]), n2, r2);
+                const float p0 = exp2_approx(a.x), p1 = exp2_approx(a.y);
+                const float p2 = exp2_approx(b.x), p3 = exp2_approx(b.y);
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
                 pb[h][nt][0] = movm_t(pack_f16(p0, p1));  // MMA rows 0-7 -> B operand (k = token, n = row)
@@ -650,6 +667,7 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     float* s_ml = s_mm + RP;
     for (int k = tid; k < kPieces; k += kT) {
         const int row = k >> 5, c = k & 31;
+        const float r = s_rows[row];
         float M = -INFINITY;
 #pragma unroll 4
         for (int w = 0; w < KW; ++w) M = fmaxf(M, s_m[w * RP + row]);
@@ -658,7 +676,7 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int w = 0; w < KW; ++w) {
-            const float f = exp2_approx(s_m[w * RP + row] - Mu);
+            const float f = exp2_approx((s_m[w * RP + row] - Mu) * r);
             const float4 v = s_o[w * kPieces + piece(row, c)];
             L += s_l[w * RP + row] * f;
             acc.x += v.x * f;
@@ -697,16 +715,17 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     for (int k0 = 0; k0 < kPieces; k0 += kT / width * n_split) {
         const int k = k0 + tid / width * n_split + split;
         const int row = k >> 5, c = k & 31;
-        float M = -INFINITY, L = 0.f;
+        float M = -INFINITY, L = 0.f, r = 1.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (sp < n_split && k < kPieces) {
+            r = s_rows[row];     // the same in every split
             M = *cl.map_shared_rank(s_mm + row, sp);
             L = *cl.map_shared_rank(s_ml + row, sp);
             acc = *cl.map_shared_rank(s_mo + piece(row, c), sp);
         }
         float Mg = M;
         for (int o = width >> 1; o > 0; o >>= 1) Mg = fmaxf(Mg, __shfl_xor_sync(0xffffffffu, Mg, o));
-        const float f = exp2_approx(M - (Mg == -INFINITY ? 0.f : Mg));
+        const float f = exp2_approx((M - (Mg == -INFINITY ? 0.f : Mg)) * r);
         L *= f;
         acc.x *= f;
         acc.y *= f;

@@ -507,3 +507,30 @@ def test_append_select_attend_run_together_and_replay():
     graph.replay()
     torch.cuda.synchronize()
     check()
+
+
+@pytest.mark.parametrize("n,hq,hkv,group", [(1, 8, 1, 1), (1, 16, 2, 4), (160, 16, 1, 1), (300, 8, 1, 1)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_of_any_size(n, hq, hkv, group, sign):
+    """Logits from 2^4 to 2^80, two values of them per row: all weight on the larger one's tokens, in
+    equal parts.  Equal K rows give equal fp32 sums, so the expected output needs no tolerance for logits."""
+    c = _case(2, hq, hkv, 1280, 16, 4, 512, group, [1201] * n, 31)
+    kc, ks = c["t"][:2]
+    kc.fill_(0x22), ks.fill_(0x38)                         # every K value 1
+    half = torch.rand(ks.shape[:-1], generator=torch.Generator(device="cuda").manual_seed(4), device="cuda") < 0.5
+    ks[half] = 0x30                                        # or 1/2
+    mag = 2.0 ** torch.linspace(4, 80, n * group * hq, device="cuda").round().view(n * group, hq)
+    c["q"] = (sign * mag[..., None]).expand(-1, -1, 128).to(torch.bfloat16).contiguous()
+    out = _attend(c)
+    for i in range(0, n * group, max(1, n // 20)):
+        tok, s = _tokens(c, i), int(c["q_seq"][i])
+        page, row = c["table"][s].long()[tok // 16], tok % 16
+        v = _values(c["t"][2][page, :, row], c["t"][3][page, :, row])
+        for h in range(hq):
+            low = half[page, h // (hq // hkv), row]
+            # 2^4: the logits differ by 2^3 x 128 x 128^-0.5 = 90, of which exp leaves nothing
+            keep = v[low if sign < 0 else ~low, h // (hq // hkv)]
+            want, size = keep.mean(0), keep.abs().mean(0)
+            # equal probabilities 2^13 and fp32 sums (2^-24 a token) below the output's rounding
+            tol = 2.0 ** -8 * want.abs() + 2.0 ** -11 * size + 2.0 ** -23
+            assert ((out[i, h].double() - want).abs() <= tol).all(), (i, h)
