@@ -16,7 +16,11 @@
 //     S = Q K^T;  P = exp2(scale log2(e) S - m);  l = l f + sum P;  O = O f + P V.
 // m only moves when a row's maximum grew by more than 8 (a factor of 256 in P, which
 // fp32 sums and bf16 P carry without loss), so the factor f is 1 in almost every step, and
-// O, which lies in TMEM, is read and written back only in the others.
+// O, which lies in TMEM, is read and written back only in the others.  An exponent is one
+// multiply-add, c S - rn(c m) with c = scale log2(e): the product's rounding is one factor of the whole
+// row and cancels, but from |c m| = 2^31 on it can leave fp32.  Two values of S that differ do so by
+// 64 or more there after the scale, so a row above 2^30 takes the power of two below c for c, whose
+// products are exact: its largest values get exponent 0 and the others at most -32.
 //
 // The grid has one CTA per item, but a CTA that finishes an item takes the next one off
 // the queue of CTAs that have not started (cluster launch control): barriers and TMEM are
@@ -72,6 +76,7 @@ constexpr uint32_t kTileBytes = kKeys * kHeadDim * 2;
 constexpr uint32_t kTmemColsPrompt = 512;
 constexpr uint32_t kColO = 256;           // TMEM column of O of tile A (S of A, S of B before it)
 constexpr float kGrow = 8.0f;             // growth of a row maximum (log2) that rescales O
+constexpr float kBig = 0x1p30f;           // scaled maximum from which a row takes a power of two for its scale
 constexpr int kEarly = 3;                 // quarters of P that the MMA may read before the last one is there
 
 enum { kPosInf = 0, kNegInf = 1, kNan = 2 };
@@ -511,7 +516,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
         const int warp_lo = i * ta + quarter * 32 / G, warp_hi = i * ta + (quarter * 32 + 31) / G;
         const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t col_s = lanes + i * kKeys, col_o = lanes + kColO + i * kHeadDim;
-        const unsigned long long sc2 = pack2(scale_log2, scale_log2);
+        const float scale_pow2 = fmaxf(__uint_as_float(__float_as_uint(scale_log2) & 0x7F800000u), 0x1p-126f);
         const bool wide = ((uintptr_t)out & 31u) == 0;     // 32-byte stores
         int n_step = 0, n_mask = 0, n_o = 0;
         Item it;
@@ -523,7 +528,8 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
             const int tok = first + row_tok;
             const int j_own = first / kKeys;               // first key tile this query tile masks
             n_mask += t.n_kv - t.j_mask;
-            float m = -INFINITY;
+            float m = -INFINITY, sc = scale_log2;          // running maximum times the row's scale, and that scale
+            auto scale_for = [&](float raw) { return fabsf(raw * scale_log2) >= kBig ? scale_pow2 : scale_log2; };
             unsigned long long l2 = 0ull;                  // two partial sums
             for (int j = 0; j < n_own; ++j, ++n_step) {
                 if (!(ok = wait_phase(&S.s_full[i], n_step & 1, err, status))) break;
@@ -557,13 +563,20 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     for (int e = 2; e < 32; e += 2)
                         mx[c] = max3(mx[c], __uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
                 }
-                const float m_new = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale_log2;
+                const float raw = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]), m_new = raw * sc;
                 const bool grow = m_new > m + kGrow;
                 if (j == 0) {
-                    m = m_new;
+                    sc = scale_for(raw);
+                    m = raw * sc;
                 } else if (__any_sync(0xffffffffu, grow)) {
-                    const float f = grow ? exp2_approx(m - m_new) : 1.0f;
-                    if (grow) m = m_new;
+                    float f = 1.0f;
+                    if (grow) {
+                        // to or from a power of two the maximum grew by 32 or more: nothing is left
+                        const float sc_new = scale_for(raw);
+                        f = sc == scale_log2 && sc_new == scale_log2 ? exp2_approx(m - m_new) : 0.f;
+                        sc = sc_new;
+                        m = raw * sc;
+                    }
                     l2 = fma2(l2, pack2(f, f), 0ull);
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
@@ -576,7 +589,7 @@ k_prompt_attn(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant_
                     }
                 }
                 const float neg = m == -INFINITY ? 0.f : -m;
-                const unsigned long long neg2 = pack2(neg, neg);
+                const unsigned long long neg2 = pack2(neg, neg), sc2 = pack2(sc, sc);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t p[16];

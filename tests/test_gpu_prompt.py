@@ -295,3 +295,30 @@ def test_values_that_are_not_finite_in_many_items(hq, hkv, n_seq, longest):
         assert qsa.qsa_read_device_status(ws) == 0
         assert torch.equal(out.isnan(), nan)
         assert torch.equal(out[~nan], want[~nan])
+
+
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (2, 2)])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_of_any_size(hq, hkv, sign):
+    """Logits from 2^4 to 2^81, two values of them per row (203 / 128 times a power of two: their scaled
+    values are rounded): all weight on the larger one's tokens, in equal parts.  Equal K rows give equal fp32 sums, so the expected output needs no tolerance for logits."""
+    n = 700
+    q, _, v = _inputs(n, hq, hkv, 19)
+    g = torch.Generator(device="cuda").manual_seed(20)
+    low = torch.rand((n, hkv), generator=g, device="cuda") < 0.5
+    k = torch.where(low, 0.5, 1.0)[..., None].expand(-1, -1, 128).to(torch.bfloat16).contiguous()
+    mag = 2.0 ** torch.randint(4, 81, (n, hq), generator=g, device="cuda")
+    q = (203 / 128 * sign * mag[..., None]).expand(-1, -1, 128).to(torch.bfloat16).contiguous()
+    out, flags = _run(q, k, v, [0, n])
+    assert flags == 0
+    for h in range(hq):
+        vv, is_low = v[:, h // (hq // hkv)].double(), low[:, h // (hq // hkv), None]
+        win = is_low if sign < 0 else ~is_low              # of two tokens that are both seen
+        some = win.cumsum(0) > 0                           # else the others are all there is
+        # 2^4: the logits differ by 2^3 x 128 x 128^-0.5 = 90, of which exp leaves nothing
+        part = lambda x: torch.where(some, (x * win).cumsum(0) / win.cumsum(0).clamp(min=1),  # noqa: E731
+                                     x.cumsum(0) / torch.arange(1, n + 1, device="cuda")[:, None])
+        want, size = part(vv), part(vv.abs())
+        # equal probabilities (each off by at most 2^-8, all alike) and fp32 sums: below the output's rounding
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -10) * size
+        assert ((out[:, h].double() - want).abs() <= tol).all(), h
