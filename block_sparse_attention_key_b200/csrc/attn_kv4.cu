@@ -293,7 +293,8 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = pack_f16(bf16lo(w[e]) * f, bf16hi(w[e]) * f);
         *reinterpret_cast<uint4*>(smem + swz_q(row, ch)) = make_uint4(h[0], h[1], h[2], h[3]);
-        if (ch == 0) s_rows[row] = __int_as_float((127 - up) << 23) * scale_log2;
+        // (not 0: a masked logit of -inf stays it; what is below 2^-126 makes every exponent 0 anyway)
+        if (ch == 0) s_rows[row] = fmaxf(__int_as_float((127 - up) << 23) * scale_log2, 0x1p-126f);
     }
     __syncthreads();  // s_seq, s_nc0, s_tlast, s_rowt, query rows
     if (tid == 0) {

@@ -534,3 +534,20 @@ def test_logits_of_any_size(n, hq, hkv, group, sign):
             # equal probabilities 2^13 and fp32 sums (2^-24 a token) below the output's rounding
             tol = 2.0 ** -8 * want.abs() + 2.0 ** -11 * size + 2.0 ** -23
             assert ((out[i, h].double() - want).abs() <= tol).all(), (i, h)
+
+
+@pytest.mark.parametrize("scale", [1e-10, 1e-18, 1e-38])
+def test_logit_scales_next_to_nothing(scale):
+    """Rows of zeros and of tiny values under a tiny scale: all logits are 0, masked places stay out."""
+    c = _case(2, 8, 2, 512, 16, 4, 512, 2, [301, 7, 130], 32)
+    c["dims"].softmax_scale = scale
+    c["q"][:, ::2] = 0
+    c["q"][:, 1::2] *= 2.0 ** -100
+    out = _attend(c)
+    for i in range(out.shape[0]):
+        tok, s = _tokens(c, i), int(c["q_seq"][i])
+        page, row = c["table"][s].long()[tok // 16], tok % 16
+        v = _values(c["t"][2][page, :, row], c["t"][3][page, :, row]).repeat_interleave(4, 1)
+        want, size = v.mean(0), v.abs().mean(0)
+        tol = 2.0 ** -8 * want.abs() + 2.0 ** -11 * size + 2.0 ** -23
+        assert ((out[i].double() - want).abs() <= tol).all(), i
