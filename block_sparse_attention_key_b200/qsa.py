@@ -472,11 +472,11 @@ def page_pools(pools, page_tokens, n_pages):
     type (K and V, or codes and scales, of every layer).  It keeps them alive; make it once."""
     if len(pools) > QSA_MAX_POOLS:
         raise ValueError(f"at most {QSA_MAX_POOLS} pools")
-    if n_pages < 1:
-        raise ValueError("at least one page expected")
+    if n_pages < 1 or page_tokens < 1:
+        raise ValueError("at least one page of at least one token expected")
     p = qsa_page_pools(len(pools), page_tokens, n_pages)
     for i, t in enumerate(pools):
-        if t.shape[0] != n_pages:
+        if t.dim() < 1 or t.shape[0] != n_pages:
             raise ValueError(f"pool {i}: {n_pages} pages expected, got {tuple(t.shape)}")
         p.pool[i] = _arg(f"pool {i}", t, t.dtype, tuple(t.shape), pools[0].get_device())
         p.page_bytes[i] = t.numel() // n_pages * t.element_size()

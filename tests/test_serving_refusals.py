@@ -288,3 +288,11 @@ def test_package_import_leaves_torch_alone():
     import sys
     code = "import sys, block_sparse_attention_key_b200; sys.exit('torch' in sys.modules)"
     assert subprocess.run([sys.executable, "-c", code], cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__)))).returncode == 0
+
+
+def test_page_pools_refuses_pages_without_tokens_and_pools_without_pages(qsa, device0):
+    for page_tokens in (0, -16):
+        with pytest.raises(ValueError, match="at least one"):
+            qsa.page_pools([_on(7, 16)], page_tokens, 7)
+    with pytest.raises(ValueError, match="pages expected"):
+        qsa.page_pools([_on()], 16, 7)
