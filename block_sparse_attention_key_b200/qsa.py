@@ -368,6 +368,8 @@ def _workspace_arg(workspace, dev):
         raise ValueError(f"workspace: tensor on {workspace.device}, but the current device is cuda:{dev}")
     if not workspace.is_contiguous():
         raise ValueError("workspace: tensors must be contiguous")
+    if workspace.nbytes < 4:
+        raise ValueError("workspace: at least the 4 bytes of the status word expected")
     return workspace.data_ptr()
 
 

@@ -28,6 +28,7 @@
  *   lengths, sequence ids and positions live on the device, so a call sequence can
  *   be captured in a CUDA graph.  Host-side integers are upper bounds used only to
  *   size grids and workspaces.
+ * - A workspace that may be NULL holds the device status word alone: 4 bytes at least.
  * - Return value: QSA_OK (0) or a negative QSA_ERR_* code.  Argument errors are
  *   detected on the host before anything is launched.  Errors the host cannot see
  *   (a device-side position outside the cache, a block index outside the bound)

@@ -296,3 +296,14 @@ def test_page_pools_refuses_pages_without_tokens_and_pools_without_pages(qsa, de
             qsa.page_pools([_on(7, 16)], page_tokens, 7)
     with pytest.raises(ValueError, match="pages expected"):
         qsa.page_pools([_on()], 16, 7)
+
+
+def test_a_workspace_holds_at_least_the_status_word(qsa, device0):
+    d = _dims(qsa, n_q_heads=1, n_kv_heads=1, batch=1)
+    rows = _on(5, 1, 128, dtype=torch.bfloat16)
+    for n in (0, 3):
+        with pytest.raises(ValueError, match="status word"):
+            qsa.qsa_prompt_attn(d, rows, rows, rows, _on(2), 5, rows, _on(n, dtype=torch.uint8))
+    p = qsa.page_pools([_on(7, 16)], 16, 7)
+    with pytest.raises(ValueError, match="status word"):
+        qsa.qsa_pages_compact(_dims(qsa), p, _on(4, 256), _on(7), _on(1), _on(0, dtype=torch.uint8))
