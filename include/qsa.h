@@ -336,7 +336,8 @@ typedef struct qsa_kv4_cache {
  * and codes 0, so they read as NaN.
  * k, v: bf16, head h of token i at element i * ld + h * head_dim (ld a multiple of 8, at
  * least n_kv_heads * head_dim).  A sequence whose bounds decrease, leave [0, n_tok] or
- * would pass kv_capacity is skipped and QSA_DEV_BAD_LEN set; a row whose page entry is
+ * would pass kv_capacity is skipped and QSA_DEV_BAD_LEN set; bounds that are out of order
+ * may keep tokens of other sequences from being appended, too.  A row whose page entry is
  * outside [0, n_pages) is skipped and QSA_DEV_BAD_PAGE set.  Pages given to two sequences
  * must not be appended to (see qsa_pages_update).
  * workspace: may be NULL (then device errors are not reported). */
@@ -422,7 +423,9 @@ int qsa_pages_compact(const qsa_dims* dims, const qsa_page_pools* pools, int32_t
  * Sequence s (of dims.batch) owns tokens [cu_len[s], cu_len[s+1]) of the packed arrays;
  * empty sequences are allowed.  Tokens before cu_len[0] and from cu_len[batch] on belong
  * to nobody: they are neither attended nor written.  A sequence whose bounds decrease or
- * leave [0, n_tok] is skipped and QSA_DEV_BAD_LEN set.
+ * leave [0, n_tok] is skipped and QSA_DEV_BAD_LEN set; where bounds are out of order, rows
+ * of other sequences may be left as they were, too, and a row that two sequences name
+ * holds one's values or the other's.
  * q, k and v may be slices of a wider array (a fused projection's output): head h of
  * token i starts at element i * ld + h * head_dim, ld a multiple of 8 and at least
  * n_heads * head_dim.  `out` must not overlap them.

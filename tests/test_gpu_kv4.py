@@ -551,3 +551,33 @@ def test_logit_scales_next_to_nothing(scale):
         want, size = v.mean(0), v.abs().mean(0)
         tol = 2.0 ** -8 * want.abs() + 2.0 ** -11 * size + 2.0 ** -23
         assert ((out[i].double() - want).abs() <= tol).all(), i
+
+
+@pytest.mark.parametrize("n_seq", [10, 40, 300])
+@pytest.mark.parametrize("bound", ["raised", "lowered", "past the rows", "negative"])
+def test_append_with_one_bad_bound_among_many_writes_only_what_some_sequence_names(n_seq, bound):
+    """BAD_LEN, and every row is its old one or that of a sequence whose own bounds are in order."""
+    g = torch.Generator().manual_seed(n_seq)
+    cap = 64
+    lens = torch.randint(1, 6, (n_seq,), generator=g).tolist()
+    start = torch.randint(0, 8, (n_seq,), generator=g).tolist()
+    cu, at = [2], n_seq // 2
+    for x in lens:
+        cu.append(cu[-1] + x)
+    n = cu[-1] + 3
+    cu[at] = {"raised": min(cu[-2], cu[at] + 40), "lowered": cu[at // 2], "past the rows": n + 1, "negative": -7}[bound]
+    x = torch.empty((n, 2, 128), dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(3))
+    dims = qsa.make_dims(n_seq, 2, 2, cap)
+    cache, t, _ = _cache(n_seq, 2, cap)
+    ws = gu.new_workspace(256)
+    _append(dims, cache, x, x, cu, start, n, ws)
+    assert qsa.qsa_read_device_status(ws) == qsa.qsa.QSA_DEV_BAD_LEN
+    rows = _quantise(x)
+    for i, got in enumerate(t):
+        got, want = got.cpu(), rows[i % 2]
+        fine = (got == 0xEE).all(-1)
+        for s, (a, b) in enumerate(zip(cu[:-1], cu[1:])):
+            if 0 <= a <= b <= n and start[s] + b - a <= cap:
+                to = slice(start[s], start[s] + b - a)
+                fine[s, :, to] |= (got[s, :, to] == want[a:b].transpose(0, 1)).all(-1)
+        assert fine.all()

@@ -322,3 +322,24 @@ def test_logits_of_any_size(hq, hkv, sign):
         # equal probabilities (each off by at most 2^-8, all alike) and fp32 sums: below the output's rounding
         tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -10) * size
         assert ((out[:, h].double() - want).abs() <= tol).all(), h
+
+
+@pytest.mark.parametrize("n_seq", [10, 40, 300])
+@pytest.mark.parametrize("bound", ["raised", "lowered", "past the rows", "negative"])
+def test_one_bad_bound_among_many_writes_only_what_some_sequence_names(n_seq, bound):
+    """BAD_LEN, and every value is its old one or that of a sequence whose own bounds are in order."""
+    g = torch.Generator().manual_seed(n_seq)
+    lens = torch.randint(1, 30, (n_seq,), generator=g).tolist()
+    cu, at = _cu(lens, first=3), n_seq // 2
+    n = cu[-1] + 5
+    cu[at] = {"raised": cu[-2], "lowered": cu[at // 2], "past the rows": n + 1, "negative": -7}[bound]
+    q, k, v = _inputs(n, 4, 2, 21)
+    out, flags = _run(q, k, v, cu)
+    assert flags == qsa.qsa.QSA_DEV_BAD_LEN
+    fine = out == 77
+    for a, b in zip(cu[:-1], cu[1:]):
+        if 0 <= a <= b <= n:
+            want, mag = _exact(q[a:b], k[a:b], v[a:b], [0, b - a])
+            tol = 2.0 ** -8 * want.abs() + (2.0 ** -8 + 2.0 ** -10) * mag + 1e-30
+            fine[a:b] |= (out[a:b].double() - want).abs() <= tol
+    assert fine.all()
