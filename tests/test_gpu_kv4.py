@@ -581,3 +581,54 @@ def test_append_with_one_bad_bound_among_many_writes_only_what_some_sequence_nam
                 to = slice(start[s], start[s] + b - a)
                 fine[s, :, to] |= (got[s, :, to] == want[a:b].transpose(0, 1)).all(-1)
         assert fine.all()
+
+
+def _exact_over(c, i, tok):
+    """_exact over given tokens of query i's sequence (paged)."""
+    s = int(c["q_seq"][i])
+    page, row = c["table"][s].long()[tok // c["page"]], tok % c["page"]
+    kc, ks, vc, vs = (t[page, :, row] for t in c["t"])
+    per = c["hq"] // c["hkv"]
+    k, v = _values(kc, ks).repeat_interleave(per, 1), _values(vc, vs).repeat_interleave(per, 1)
+    p = torch.softmax(torch.einsum("thd,hd->ht", k, c["q"][i].double()) * 128 ** -0.5, 1)
+    return torch.einsum("ht,thd->hd", p, v), torch.einsum("ht,thd->hd", p, v.abs())
+
+
+@pytest.mark.parametrize("group", [1, 3])
+@pytest.mark.parametrize("entry", [-1, 1 << 20, -(1 << 31)])
+@pytest.mark.parametrize("place", [0, 18])
+def test_tokens_of_a_page_that_is_not_there_are_left_out(place, entry, group):
+    """A selected page, or the one of the tail: the sequence's queries attend their other tokens, the other
+    sequences' give the same bits."""
+    c = _case(2, 8, 2, 512, 16, 4, 512, group, [297, 290, 299, 120], 33)
+    good = _attend(c)
+    c["table"][0, place] = entry
+    out = _attend(c, qsa.qsa.QSA_DEV_BAD_PAGE)
+    for i in range(out.shape[0]):
+        if int(c["q_seq"][i]) == 1:
+            assert torch.equal(out[i], good[i])
+            continue
+        tok = _tokens(c, i)
+        tok = tok[tok // 16 != place]
+        want, mag = _exact_over(c, i, tok)
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -11) * mag + 2.0 ** -23
+        assert ((out[i].double() - want).abs() <= tol).all(), i
+
+
+@pytest.mark.parametrize("batch,group,hq,hkv", [(1, 1, 8, 1), (6, 2, 16, 2), (16, 1, 32, 4), (64, 1, 32, 4), (200, 3, 8, 2)])
+def test_same_inputs_give_the_same_bits_whatever_runs_beside(batch, group, hq, hkv):
+    """A cache per sequence, from split lists to many; the calls of two streams overlap."""
+    g = torch.Generator().manual_seed(batch)
+    t0s = torch.randint(200, 2400, (batch,), generator=g).tolist()
+    c = _case(batch, hq, hkv, 2560, 64, 4, 512, group, t0s, batch)
+    first = _attend(c)
+    _compare(c, first, rows=range(0, batch * group, max(1, batch * group // 12)))
+    outs = [torch.empty_like(first) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for out, st in zip(outs, streams):
+            qsa.qsa_sparse_attn_kv4(c["dims"], c["cache"], c["q"], c["q_seq"], c["q_pos"], c["sel"], c["cnt"],
+                                    first.shape[0], out, group_q=group, stream=st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], first) and torch.equal(outs[1], first)
