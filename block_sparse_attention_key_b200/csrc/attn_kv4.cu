@@ -47,7 +47,7 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
-#include "qsa_internal.cuh"
+#include "sm100_ptx.cuh"
 
 namespace qsa {
 
@@ -98,23 +98,10 @@ __device__ __forceinline__ void cp_async8(uint32_t saddr, const void* g, int src
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;\n" ::"r"(saddr), "l"(g), "r"(src_bytes));
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::); }
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// two fp32 in one register pair, and (s + n) * r + kProbShift of both: two instructions
-__device__ __forceinline__ unsigned long long pair(float lo, float hi)
-{
-    return ((unsigned long long)__float_as_uint(hi) << 32) | __float_as_uint(lo);
-}
+// (s + n) * r + kProbShift of two fp32 each
 __device__ __forceinline__ float2 shifted2(unsigned long long s, unsigned long long n, unsigned long long r)
 {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(s), "l"(n));
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(d), "l"(r), "l"(pair(kProbShift, kProbShift)));
+    const unsigned long long d = sm100::fma2(sm100::add2(s, n), r, sm100::pack2(kProbShift, kProbShift));
     return make_float2(__uint_as_float((unsigned)d), __uint_as_float((unsigned)(d >> 32)));
 }
 
@@ -188,12 +175,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;\n" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
 
@@ -546,11 +527,11 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         uint32_t pb[2][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const unsigned long long r2 = pair(rsc[nt][0], rsc[nt][1]), n2 = pair(neg[nt][0], neg[nt][1]);
+            const unsigned long long r2 = sm100::pack2(rsc[nt][0], rsc[nt][1]), n2 = sm100::pack2(neg[nt][0], neg[nt][1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float2 a = shifted2(pair(sc[h][nt][0], sc[h][nt][1]), n2, r2);
-                const float2 b = shifted2(pair(sc[h][nt][2], sc[h][nt][3]), n2, r2);
+                const float2 a = shifted2(sm100::pack2(sc[h][nt][0], sc[h][nt][1]), n2, r2);
+                const float2 b = shifted2(sm100::pack2(sc[h][nt][2], sc[h][nt][3]), n2, r2);
                 const float p0 = exp2_approx(a.x), p1 = exp2_approx(a.y);
                 const float p2 = exp2_approx(b.x), p3 = exp2_approx(b.y);
                 l[nt][0] += p0 + p2;
@@ -698,8 +679,8 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
         const float inv = L == 0.f ? 0.f : 1.f / L;   // a row that attends nothing is 0; a NaN sum stays NaN
         uint2 v = make_uint2(0u, 0u);                 // and so is one of a skipped query
         if (s_rowt[row] >= 0) {
-            v.x = pack_bf16(a.x * inv, a.y * inv);
-            v.y = pack_bf16(a.z * inv, a.w * inv);
+            v.x = pack_bf16x2(a.x * inv, a.y * inv);
+            v.y = pack_bf16x2(a.z * inv, a.w * inv);
         }
         *reinterpret_cast<uint2*>(out + ((qi0 + row / G) * n_q_heads + (int64_t)g * G + row % G) * kHeadDim + 4 * c) = v;
     };
@@ -711,7 +692,7 @@ k_sparse_attn_kv4(const uint4* __restrict__ q, const uint8_t* __restrict__ k_cod
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
     // `width` lanes per piece, one per split, so that a share takes one round trip to the others
-    const int width = n_split <= 2 ? 2 : n_split <= 4 ? 4 : n_split <= 8 ? 8 : 16;
+    const int width = n_split <= 2 ? 2 : n_split <= 4 ? 4 : 8;
     const int sp = tid & (width - 1);
     for (int k0 = 0; k0 < kPieces; k0 += kT / width * n_split) {
         const int k = k0 + tid / width * n_split + split;

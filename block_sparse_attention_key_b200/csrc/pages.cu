@@ -127,7 +127,9 @@ k_pages_update(int32_t* table, int32_t* ref, int batch, int table_ld, int page_t
     __shared__ int s_moves;
     __shared__ int s_at[kPlanThreads], s_lo[kPlanThreads], s_lb[kPlanThreads];
     const int tid = threadIdx.x;
-    griddep_launch_dependents();   // the mover waits for this kernel's end before it reads anything
+    // before any wait, against the rule at launch_k: this kernel is itself launched without a programmatic
+    // dependency, so all that is older has ended, and the mover waits for its end before it reads anything
+    griddep_launch_dependents();
     if (tid == 0) s_moves = 0;
 
     // ---- free: a place is emptied by whoever swaps its entry out, so a sequence may be named twice ----

@@ -103,27 +103,6 @@ struct __align__(1024) PromptSmem {
     int error, any_bad[2];                         // any_bad: a mark of `bad` is set, per dim half
 };
 
-__device__ __forceinline__ float exp2_approx(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b)
-{
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // Take the next CTA of the grid that has not started; 16 bytes of answer arrive on `bar`.
 __device__ __forceinline__ void take_next_cta(uint4* answer, uint64_t* bar)
 {
