@@ -31,9 +31,9 @@
 // than 2 (probabilities then reach 2^16 / 2, inside fp16), so accumulators are rescaled,
 // and lanes compare their maxima at all, in few steps.
 //
-// Measured: 1,024 queries of 2,052 tokens at 32 / 4 heads 261 us (issue slots 68%, ALU pipe
+// Measured: 1,024 queries of 2,052 tokens at 32 / 4 heads 263 us (issue slots 68%, ALU pipe
 // 58% busy: one conversion per two values is what the format costs); a decode step of 16 x
-// 64K contexts 11.6 us (18.9 MB), of one 8K context with two drafts 9.8 us: round trips and
+// 64K contexts 12.2 us (18.9 MB), of one 8K context with two drafts 10.4 us: round trips and
 // one pass through code that is not in the instruction cache yet.
 //
 // Masked places: absent tokens are zero-filled and their logits -inf.  A scale may be NaN
@@ -742,6 +742,8 @@ int nt_for(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 //   400 lists 56.6 / 45.1 / 58.0, 2,368 lists 294 / 222 / 224
 //   <= 32 rows, 8 / 4 / 2 warps: 148 lists 33.3 / 41.9 / 72.5, 149 lists 59.9 / 52.7 / 73.3,
 //   400 lists 92 / 90 / 97, 2,368 lists 483 / 405 / 384
+// Two warps were only tried: the 2 to 5% that they are ahead at thousands of lists are paid for by
+// up to 40% at 150 to 400, and a third kernel per row tile count would have to be kept for them.
 int tier4(int64_t lists) { return lists <= 148 ? 0 : lists <= 296 ? 1 : 2; }
 
 struct Shape {

@@ -13,8 +13,10 @@
 //
 // Bytes only: 256 read and 72 written per row.  One thread per block of 16 (two 16-byte
 // loads, one 8-byte store of codes, 8 threads fill a row's 8 scale bytes), rows in the
-// order of the packed input, so reads are contiguous.  8,192 tokens of 8 KV heads (42 MB
-// read, 8 written): 13.6 us with cold caches; with a division per value it was 17.5.
+// order of the packed input, so reads are contiguous.  8,192 tokens of 8 KV heads (33.6 MB
+// read, 9.4 written: 6.5 us at the copy rate): 13.4 us with cold caches; with a division per value
+// it was 17.5.  What is left is the short CTAs' waves, a search for the sequence per row, and
+// scales written 8 bytes at a time.
 
 #include "qsa_internal.cuh"
 

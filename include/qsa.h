@@ -346,7 +346,7 @@ int qsa_kv4_append(const qsa_dims* dims, const qsa_kv4_cache* cache, const void*
                    void* stream);
 
 /* Step 4 over such a cache: qsa_sparse_attn_ex's arguments, rules and result, K and V
- * being the cache's values (k_cache, v_cache and the page fields of `args` must be NULL
+ * being the cache's values, the probabilities rounded to fp16 (k_cache, v_cache and the page fields of `args` must be NULL
  * and 0: the cache holds them).  A row that attends nothing is 0.  No scratch: workspace
  * may be NULL (then device errors are not reported). */
 int qsa_sparse_attn_kv4(const qsa_dims* dims, const qsa_kv4_cache* cache, const qsa_attn_args* args, void* workspace,
@@ -366,7 +366,11 @@ int qsa_attn_kv4_plan(const qsa_dims* dims, int32_t n_q, int32_t group_q, qsa_at
  * `pools` names them all (K and V, or codes and scales, of each layer), page p of pool i
  * being bytes [p * page_bytes[i], (p + 1) * page_bytes[i]) (page_bytes a multiple of 16, at
  * most 2^31).  At most 2^30 pages, table entries, and entries of the sequences that one call
- * frees or forks. */
+ * frees or forks.
+ * A table's calls have to name all its arrays: the call that changes the table moves the
+ * contents, and a second one finds nothing left to move.  More than QSA_MAX_POOLS arrays (32
+ * layers of a 4-bit cache, 64 of a bf16 one) need a table and counts for each group of so
+ * many, and a call for each. */
 #define QSA_MAX_POOLS 128
 
 typedef struct qsa_page_pools {
@@ -418,7 +422,8 @@ int qsa_pages_compact(const qsa_dims* dims, const qsa_page_pools* pools, int32_t
  * out[i][h] = sum_{j <= i} softmax_j(scale * q[i][h].k[j][g]) v[j][g], j over the tokens
  * of query token i's own sequence: what the layer computes while a prompt is shorter
  * than its budget, and what a model's dense GQA layers compute at any length.  fp32
- * logits, softmax and accumulation; bf16 output (RNE).
+ * logits, softmax and accumulation; the probabilities are rounded to bf16 for the product
+ * with v (their sum is not); bf16 output (RNE).
  *
  * Sequence s (of dims.batch) owns tokens [cu_len[s], cu_len[s+1]) of the packed arrays;
  * empty sequences are allowed.  Tokens before cu_len[0] and from cu_len[batch] on belong
